@@ -349,6 +349,74 @@ fp8q_status fp8q_permute_pad_quant_noalloc(const void *x, int64_t tokens, int64_
                                            int32_t align, uint8_t *q, uint8_t *sf, int64_t max_out_rows,
                                            int32_t *expert_offsets, int32_t *row_id_map, fp8q_stream_t stream);
 
+/* ------------------------------------------------------------------ router
+ * The router in front of the permute: which experts a token goes to, with which weights,
+ * and the balance loss that keeps them evenly used.  For logits l[t, e]:
+ *   p = softmax(l[t, :]), or with FP8Q_ROUTER_SIGMOID p_e = 1 / (1 + exp(-l_e));
+ *   topk_idx[t, :] = the topk experts of largest l (with `bias`: of largest p_e + bias_e,
+ *     formed in double), largest first, equal ones by lowest id: always distinct ids in
+ *     [0, num_experts), as the permutes need them;
+ *   weights[t, s] = scale * p_i for i = topk_idx[t, s], with FP8Q_ROUTER_RENORM divided by
+ *     (sum of the topk chosen p + 1e-20).  The bias takes part in the choice alone.
+ * Balance statistics over the tokens with token_mask[t] != 0 (NULL: all tokens):
+ *   counts[e] = pairs routed to e;  prob_sums[e] = sum over t of p_te (softmax) or
+ *   p_te / (sum_j p_tj + 1e-20) (sigmoid);  with C = sum of counts,
+ *   loss = loss_coef * num_experts * topk / C^2 * sum_e counts[e] * prob_sums[e]   (0 if C == 0),
+ * which is loss_coef * E * sum_e f_e * P_e with f_e the share of the pairs and P_e the mean
+ * probability of e.
+ *   logits     : fp32 [tokens, num_experts], or BF16 with FP8Q_ROUTER_BF16.  -inf switches
+ *                an expert off (p = 0; it is chosen only when fewer than topk others are
+ *                left, with weight 0).  NaN counts as -inf, +inf as the largest finite
+ *                value.  A row of -inf alone gets ids 0..topk-1 with weights 0.
+ *   bias       : fp32 [num_experts], only with FP8Q_ROUTER_SIGMOID, or NULL.
+ *   token_mask : u8 [tokens] or NULL.  A token with 0 (padding) still gets valid ids, its
+ *                weights are 0, and it takes no part in the statistics and the gradient.
+ *   topk_idx   : out int32 [tokens, topk];  weights : out fp32 [tokens, topk].
+ *   counts, prob_sums, loss : out int32 [num_experts], fp32 [num_experts], fp32 [1]; all
+ *                given, or all NULL (serving: no statistics, no workspace).
+ *   workspace  : device, >= fp8q_router_workspace_bytes(tokens, num_experts), 16-byte
+ *                aligned; scratch of this call alone (calls that share one and overlap race).
+ *   num_experts in [1, 1024]; topk in [1, min(64, num_experts)]; tokens*topk at most
+ *   2^31 - 1.  tokens == 0 writes the statistics (zeros).  Results do not depend on timing:
+ *   every sum has a fixed order.  Errors: NULL, ALIGN, SHAPE, ARG, CUDA.
+ *
+ * fp8q_router_topk_bwd: the gradient of the logits, from the gradients of the weights and
+ * of the loss; the ids, the counts and the bias carry none.
+ *   grad_weights : fp32 [tokens, topk], or NULL (no gradient from the weights).  With
+ *                  row_id_map (int32 [tokens, topk], from a permute) it is fp32
+ *                  [grad_rows] in the permute's row order instead, and pair (t, s) reads
+ *                  grad_weights[row_id_map[t, s]] (as fp8q_swiglu_bwd returns them).
+ *   counts       : as fp8q_router_topk wrote them (or summed over the ranks of a job);
+ *   grad_loss    : fp32 [1] on the device, or NULL (no gradient from the loss; counts may
+ *                  then be NULL).
+ *   topk_idx     : needed with grad_weights.  An id outside [0, num_experts), or a row id
+ *                  outside [0, grad_rows), sets FP8Q_ERR_DEVICE in the status word and its
+ *                  slot is skipped.
+ *   grad_logits  : out, the logits' type and shape; every element is written (0 for a
+ *                  masked token).  logits, flags, token_mask, topk, scale, loss_coef: as in
+ *                  the forward call.  May not alias logits. */
+#define FP8Q_ROUTER_SIGMOID 0x1u /* scores are sigmoids, not a softmax */
+#define FP8Q_ROUTER_RENORM 0x2u  /* weights divided by the sum of the chosen ones */
+#define FP8Q_ROUTER_BF16 0x4u    /* logits (and their gradient) are BF16, not fp32 */
+size_t fp8q_router_workspace_bytes(int64_t tokens, int32_t num_experts);
+fp8q_status fp8q_router_topk(const void *logits, int64_t tokens, int32_t num_experts, uint32_t flags,
+                             const float *bias, const uint8_t *token_mask, int32_t topk, float scale,
+                             float loss_coef, int32_t *topk_idx, float *weights, int32_t *counts, float *prob_sums,
+                             float *loss, void *workspace, size_t workspace_bytes, fp8q_stream_t stream);
+fp8q_status fp8q_router_topk_bwd(const void *logits, int64_t tokens, int32_t num_experts, uint32_t flags,
+                                 const uint8_t *token_mask, int32_t topk, float scale, const int32_t *topk_idx,
+                                 const float *grad_weights, const int32_t *row_id_map, int64_t grad_rows,
+                                 const int32_t *counts, float loss_coef, const float *grad_loss, void *grad_logits,
+                                 fp8q_stream_t stream);
+
+/* Routing weights in the permute's row order: row_weights[row_id_map[i]] = weights[i] for
+ * i < pairs, every other of the `rows` rows 0 (padding rows therefore get weight 0).
+ *   weights fp32 [pairs]; row_id_map int32 [pairs], as a permute wrote it (an entry outside
+ *   [0, rows) sets FP8Q_ERR_DEVICE and is skipped); row_weights out fp32 [rows].
+ * Errors: NULL, ALIGN, SHAPE, CUDA. */
+fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id_map, int64_t pairs, int64_t rows,
+                                     float *row_weights, fp8q_stream_t stream);
+
 /* Test hook for the bounded-wait machinery (no counterpart on the pages): launches one
  * CTA that waits on an mbarrier nobody arrives at, giving up after `timeout_ns`
  * nanoseconds (clamped to [1e3, 2e9]); the kernel then records FP8Q_ERR_TIMEOUT in the

@@ -51,6 +51,7 @@ def lib() -> ctypes.CDLL:
                                "`python -m scaling_aware_transpose_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+        F32 = ctypes.c_float
         sig = {
             "fp8q_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "fp8q_last_device_status": ([P], ctypes.c_int),
@@ -78,6 +79,12 @@ def lib() -> ctypes.CDLL:
             "fp8q_ep_recv_workspace_bytes": ([I64, I32, I32], SZ),
             "fp8q_ep_recv_permute_fp8": ([ctypes.POINTER(EpSource), I32, I64, I32, I32, I32, P, P, I64, P, P, P, SZ,
                                           P], ctypes.c_int),
+            "fp8q_router_workspace_bytes": ([I64, I32], SZ),
+            "fp8q_router_topk": ([P, I64, I32, ctypes.c_uint32, P, P, I32, F32, F32, P, P, P, P, P, P, SZ, P],
+                                 ctypes.c_int),
+            "fp8q_router_topk_bwd": ([P, I64, I32, ctypes.c_uint32, P, I32, F32, P, P, P, I64, P, F32, P, P, P],
+                                     ctypes.c_int),
+            "fp8q_permute_row_weights": ([P, P, I64, I64, P, P], ctypes.c_int),
             "fp8q_version": ([], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -469,3 +476,7 @@ def ep_recv_permute(segments, experts_per_rank: int, align: int, max_out_rows: i
     fp8q_ep_recv_permute_fp8([(a, b, c, a.shape[0]) for a, b, c in segments], hidden, topk, experts_per_rank, align,
                              q, sf, max_out_rows, off, rmap, ws, ws.numel(), stream)
     return q, sf, off, rmap[:rows * topk]
+
+
+# ---------------------------------------------------------------- router, 8-bit checkpoints, MXFP4 products
+from .moe import *  # noqa: E402,F401,F403

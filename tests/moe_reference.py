@@ -1,0 +1,87 @@
+"""Plain 64-bit forms of the router, the SwiGLU backward and the 4-bit quantization, from
+their definitions (numpy float64 on the host), and the error bounds of their fp32 kernels."""
+import numpy as np
+
+U = 2.0 ** -24      # half a step of fp32, relative
+U_BF16 = 2.0 ** -8  # half a step of BF16, relative
+
+
+def clean(logits):
+    l = np.asarray(logits, np.float64).copy()
+    l[np.isnan(l)] = -np.inf
+    return np.minimum(l, np.finfo(np.float32).max)
+
+
+def router(logits, topk, sigmoid=False, renorm=True, bias=None, mask=None, scale=1.0, loss_coef=1.0):
+    """dict(idx, weights, counts, sums, loss, p, h, P) in float64."""
+    l = clean(logits)
+    T, E = l.shape
+    live = np.ones(T, bool) if mask is None else np.asarray(mask) != 0
+    with np.errstate(all="ignore"):
+        if sigmoid:
+            p = 1.0 / (1.0 + np.exp(-l))
+            h = p / (p.sum(1, keepdims=True) + 1e-20)
+        else:
+            m = l.max(1, keepdims=True)
+            x = np.exp(l - np.where(np.isinf(m), 0.0, m))
+            z = x.sum(1, keepdims=True)
+            p = x / np.where(z == 0, 1.0, z)
+            h = p
+    key = p + np.asarray(bias, np.float64) if bias is not None else l
+    idx = np.argsort(-key, axis=1, kind="stable")[:, :topk]
+    pk = np.take_along_axis(p, idx, 1)
+    P = pk.sum(1, keepdims=True) + 1e-20 if renorm else np.ones((T, 1))
+    w = np.where(live[:, None], scale * pk / P, 0.0)
+    counts = np.bincount(idx[live].reshape(-1), minlength=E)
+    sums = h[live].sum(0)
+    C = float(counts.sum())
+    coef = loss_coef * E * topk / C ** 2 if C else 0.0
+    return dict(idx=idx, weights=w, counts=counts, sums=sums, loss=coef * float((counts * sums).sum()), p=p, h=h, P=P,
+                live=live, coef=coef)
+
+
+def router_bwd(logits, idx, grad_weights, counts, grad_loss, sigmoid=False, renorm=True, mask=None, scale=1.0,
+               loss_coef=1.0):
+    """(gradient of the logits, a magnitude bound of what was added up to form it)."""
+    T, E = np.asarray(logits).shape
+    K = idx.shape[1]
+    r = router(logits, K, sigmoid, renorm, None, mask, scale, loss_coef)
+    p, h = r["p"], r["h"]
+    pk = np.take_along_axis(p, idx, 1)
+    P = pk.sum(1, keepdims=True) + 1e-20 if renorm else np.ones((T, 1))
+    d = np.zeros((T, E))
+    A = np.zeros((T, E))
+    if grad_weights is not None:
+        gw = np.asarray(grad_weights, np.float64)
+        mean = (gw * pk).sum(1, keepdims=True) / P if renorm else 0.0
+        mean_abs = (np.abs(gw) * pk).sum(1, keepdims=True) / P if renorm else 0.0
+        t = np.arange(T)[:, None].repeat(K, 1)
+        np.add.at(d, (t, idx), scale * (gw - mean) / P)
+        np.add.at(A, (t, idx), abs(scale) * (np.abs(gw) + mean_abs) / P)
+    g = np.zeros(E)
+    if grad_loss is not None:
+        C = float(np.sum(counts))
+        g = float(grad_loss) * loss_coef * E * K / C ** 2 * np.asarray(counts, np.float64) if C else g
+    if sigmoid:
+        z = p.sum(1, keepdims=True) + 1e-20
+        with np.errstate(over="ignore"):
+            q = 1.0 / (1.0 + np.exp(clean(logits)))
+        out = (d + (g - (g * h).sum(1, keepdims=True)) / z) * p * q
+        A = (A + (np.abs(g) + (np.abs(g) * h).sum(1, keepdims=True)) / z) * p * q
+    else:
+        d = d + g
+        A = A + np.abs(g)
+        out = p * (d - (d * p).sum(1, keepdims=True))
+        A = p * (A + (A * p).sum(1, keepdims=True))
+    live = r["live"][:, None]
+    return np.where(live, out, 0.0), np.where(live, A, 0.0)
+
+
+def router_units(logits):
+    """How many half steps of fp32 (U) a probability may be off: the rounding of l - max
+    (|l - max| half steps of the exponent's argument), expf (2 steps = 4 U), a warp's sum
+    (up to 32 + 5 additions), the reciprocal and products (8)."""
+    l = clean(logits)
+    fin = l[np.isfinite(l) & (np.abs(l) < 1e30)]
+    span = float(fin.max() - fin.min()) if fin.size else 0.0
+    return span + 4 + 37 + 8
