@@ -417,6 +417,45 @@ fp8q_status fp8q_router_topk_bwd(const void *logits, int64_t tokens, int32_t num
 fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id_map, int64_t pairs, int64_t rows,
                                      float *row_weights, fp8q_stream_t stream);
 
+/* ------------------------------------------------------------------ 8-bit SwiGLU checkpoints
+ * Training form of the SwiGLU: what the backward pass needs of gate and up is kept as
+ * 8-bit codes (2 B per element pair and scales instead of 4 B of BF16), quantized from the
+ * same read.
+ *
+ * fp8q_swiglu_quant_stash: y = silu(gate) * up as in fp8q_swiglu_quant, times
+ * row_weights[row] when given (one more fp32 rounding; a routing weight carried here makes
+ * the combine an unweighted sum).
+ *   q, sf, qt, sft : as fp8q_swiglu_quant (qt, sft both NULL or both given); without
+ *                    row_weights byte for byte its results.
+ *   gq, gsf, uq, usf : out, the row-wise pairs of fp8q_quantize_rowwise(gate) and (up).
+ *   row_weights    : fp32 [rows] or NULL (all ones); finite.
+ *
+ * fp8q_swiglu_bwd: with g, u decoded from the codes, s = 1 / (1 + exp(-g)) and w the row's
+ * weight (1 if row_weights is NULL), from dy, the gradient of y (BF16 [rows, cols]):
+ *   dgate = dy*w*u*s*(1 + g*(1 - s)),  dup = dy*w*g*s     (out, BF16 [rows, cols]),
+ *   drow_weights[row] = sum over the row of dy*g*s*u      (out, fp32 [rows], or NULL; only
+ *                       with row_weights), summed in a fixed order.
+ * fp8q_swiglu_bwd_quant: the same gradients as row-wise E4M3 pairs (dgq, dgsf), (duq, dusf)
+ * by the rule of fp8q_quantize_rowwise applied to the fp32 values, ready for the FP8 products and
+ * fp8q_direct_transpose (dense or grouped); with yq, ysf (both or neither) also y = g*s*u*w
+ * recomputed from the codes, so that the forward's q need not be kept.
+ *
+ * All: cols % 128 == 0, any rows >= 0; codes and BF16 arrays 16-byte aligned; outputs may
+ * not alias inputs.  The codes must come from a quantization (never 0x7F/0xFF).  A product
+ * outside fp32's range is the caller's (inputs of ordinary size have none).
+ * Errors: NULL, ALIGN, SHAPE, ARG (only one of a pair, drow_weights without row_weights),
+ * CUDA. */
+fp8q_status fp8q_swiglu_quant_stash(const void *gate, const void *up, const float *row_weights, int64_t rows,
+                                    int64_t cols, uint8_t *q, uint8_t *sf, uint8_t *qt, uint8_t *sft, uint8_t *gq,
+                                    uint8_t *gsf, uint8_t *uq, uint8_t *usf, fp8q_stream_t stream);
+fp8q_status fp8q_swiglu_bwd(const uint8_t *gq, const uint8_t *gsf, const uint8_t *uq, const uint8_t *usf,
+                            const float *row_weights, const void *dy, int64_t rows, int64_t cols, void *dgate,
+                            void *dup, float *drow_weights, fp8q_stream_t stream);
+fp8q_status fp8q_swiglu_bwd_quant(const uint8_t *gq, const uint8_t *gsf, const uint8_t *uq, const uint8_t *usf,
+                                  const float *row_weights, const void *dy, int64_t rows, int64_t cols, uint8_t *dgq,
+                                  uint8_t *dgsf, uint8_t *duq, uint8_t *dusf, uint8_t *yq, uint8_t *ysf,
+                                  float *drow_weights, fp8q_stream_t stream);
+
 /* Test hook for the bounded-wait machinery (no counterpart on the pages): launches one
  * CTA that waits on an mbarrier nobody arrives at, giving up after `timeout_ns`
  * nanoseconds (clamped to [1e3, 2e9]); the kernel then records FP8Q_ERR_TIMEOUT in the

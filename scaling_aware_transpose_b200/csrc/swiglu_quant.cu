@@ -40,6 +40,12 @@
 // each thread holds two passes of gate/up in registers and, as it consumes one, loads the
 // pass two ahead (crossing into its next block), so one pass of loads is in flight per
 // thread while it computes the other.
+//
+// Training variant (Stash): gate and up are kept for the backward pass as 8-bit codes
+// (fp8q_swiglu_bwd, swiglu_bwd.cu).  They are quantized by the same 1x128 rule from the
+// registers that already hold them, so the two extra outputs cost 2 B of writes and no
+// read per element; y may carry one fp32 factor per row (the routing weight).
+#include "abi_checks.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -214,17 +220,37 @@ __device__ __forceinline__ void load_pass(BlockIn& in, int p, const uint16_t* __
   }
 }
 
+// The training variant's extra operands (all NULL in the plain kernel).
+struct StashArgs {
+  const float* row_weights;  // [rows] or NULL
+  uint8_t *gq, *gsf, *uq, *usf;
+};
+
+// 16 bf16 of one lane of a tile's eight -> 16 codes and the tile's scale byte, by the
+// row-wise rule.
+__device__ __forceinline__ uint4 quantize16(const uint32_t (&w)[8], int& e) {
+  uint32_t m = maxabs_bf16x2(maxabs_bf16x2(maxabs_bf16x2(w[0], w[1]), maxabs_bf16x2(w[2], w[3])),
+                             maxabs_bf16x2(maxabs_bf16x2(w[4], w[5]), maxabs_bf16x2(w[6], w[7])));
+  m = maxabs_bf16x2(m, __byte_perm(m, 0u, 0x1032)) & 0x7FFFu;
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  e = bf16_tile_exponent(m);
+  const float s = exp2_neg(e);
+  return make_uint4(encode4(w[0], w[1], s), encode4(w[2], w[3], s), encode4(w[4], w[5], s), encode4(w[6], w[7], s));
+}
+
+template <bool Stash>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) swiglu_quant_kernel(const uint16_t* __restrict__ gate,
                                                                          const uint16_t* __restrict__ up, int64_t rows,
                                                                          int cols, int nblk,
                                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                                          uint8_t* __restrict__ qt,
-                                                                         uint8_t* __restrict__ sft) {
+                                                                         uint8_t* __restrict__ sft, StashArgs st) {
   __shared__ __align__(16) float silu_tab[kTabPad];
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ __align__(16) uint8_t e_row[128];
   __shared__ int e_max_sh;
-  pdl_wait_for(gate, up);
+  pdl_wait_for(gate, up, st.row_weights);
   pdl_trigger();
   const int tid = threadIdx.x;
   const int ncb = cols >> 7;
@@ -267,6 +293,23 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) swiglu_quant_kernel(cons
 #pragma unroll
       for (int k = 0; k < 8; ++k)  // y = silu(g) * u
         mul2_rn(y[2 * k], y[2 * k + 1], __uint_as_float(uw[k] << 16), __uint_as_float(uw[k] & 0xFFFF0000u));
+      if (Stash) {
+        int eg, eu;
+        const uint4 cg = quantize16(gw, eg), cu = quantize16(uw, eu);
+        if (r < rows) {
+          *reinterpret_cast<uint4*>(st.gq + r * cols + c0 + sub * 16) = cg;
+          *reinterpret_cast<uint4*>(st.uq + r * cols + c0 + sub * 16) = cu;
+          if (sub == 0) {
+            st.gsf[r * ncb + (c0 >> 7)] = (uint8_t)(eg + 127);
+            st.usf[r * ncb + (c0 >> 7)] = (uint8_t)(eu + 127);
+          }
+        }
+        if (st.row_weights != nullptr) {
+          const float w = r < rows ? ld_g(st.row_weights + r) : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mul2_rn(y[2 * k], y[2 * k + 1], w, w);
+        }
+      }
       float amax;  // finite y: the largest magnitude, by three-input max instructions
       {
         const float a0 = max3abs(y[0], y[1], y[2]), a1 = max3abs(y[3], y[4], y[5]), a2 = max3abs(y[6], y[7], y[8]);
@@ -379,17 +422,28 @@ __global__ void __launch_bounds__(kThreads) silu_table_kernel(const uint32_t* __
 
 }  // namespace
 
-fp8q_status launch_swiglu_quant(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
-                                uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, cudaStream_t stream) {
+namespace {
+
+fp8q_status launch_swiglu(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
+                          uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, bool stash, const StashArgs& st,
+                          cudaStream_t stream) {
   if (rows == 0 || cols == 0) return FP8Q_OK;
   const int64_t nblk = (rows + 127) / 128 * (cols / 128);
   if (nblk > 0x7FFFFFFF - 0x10000) return FP8Q_ERR_SHAPE;  // block indices are int32
   const int64_t slots = (int64_t)dev.num_sms * kMinBlocks;
   const int64_t grid = nblk < slots ? nblk : slots;
-  return launch_after(swiglu_quant_kernel, dim3((unsigned)grid), kThreads, 0, stream, static_cast<const uint16_t*>(gate),
-                      static_cast<const uint16_t*>(up), rows, (int)cols, (int)nblk, q, sf, qt, sft) == cudaSuccess
+  return launch_after(stash ? swiglu_quant_kernel<true> : swiglu_quant_kernel<false>, dim3((unsigned)grid), kThreads, 0,
+                      stream, static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(up), rows, (int)cols,
+                      (int)nblk, q, sf, qt, sft, st) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
+}
+
+}  // namespace
+
+fp8q_status launch_swiglu_quant(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
+                                uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, cudaStream_t stream) {
+  return launch_swiglu(dev, gate, up, rows, cols, q, sf, qt, sft, false, StashArgs{}, stream);
 }
 
 fp8q_status launch_debug_exp_spec_range(uint32_t first, int64_t n, float* out, cudaStream_t stream) {
@@ -411,3 +465,23 @@ fp8q_status launch_debug_silu_bf16(const void* g, int64_t n, float* y, cudaStrea
 }
 
 }  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8q_status fp8q_swiglu_quant_stash(const void* gate, const void* up, const float* row_weights, int64_t rows,
+                                               int64_t cols, uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft,
+                                               uint8_t* gq, uint8_t* gsf, uint8_t* uq, uint8_t* usf,
+                                               fp8q_stream_t stream) {
+  if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxInt32 || cols > kMaxInt32) return FP8Q_ERR_SHAPE;
+  if ((qt == nullptr) != (sft == nullptr)) return FP8Q_ERR_ARG;
+  if (qt && rows % 128) return FP8Q_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  if (!gate || !up || !q || !sf || !gq || !gsf || !uq || !usf) return FP8Q_ERR_NULL;
+  if (!aligned_to(gate, 16) || !aligned_to(up, 16) || !aligned_to(q, 16) || !aligned_to(gq, 16) ||
+      !aligned_to(uq, 16) || !aligned_to(qt, 4) || !aligned_to(row_weights, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo dev;
+  if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
+  return launch_swiglu(dev, gate, up, rows, cols, q, sf, qt, sft, true, StashArgs{row_weights, gq, gsf, uq, usf},
+                       to_stream(stream));
+}

@@ -13,6 +13,8 @@ from . import _check, _stream, lib
 __all__ = [
     "ROUTER_SIGMOID", "ROUTER_RENORM", "ROUTER_BF16", "fp8q_router_workspace_bytes", "fp8q_router_topk",
     "fp8q_router_topk_bwd", "fp8q_permute_row_weights", "router_topk", "router_topk_bwd", "permute_row_weights",
+    "fp8q_swiglu_quant_stash", "fp8q_swiglu_bwd", "fp8q_swiglu_bwd_quant", "swiglu_quant_stash", "swiglu_bwd",
+    "swiglu_bwd_quant",
 ]
 
 ROUTER_SIGMOID = 0x1  # FP8Q_ROUTER_SIGMOID
@@ -159,3 +161,98 @@ def permute_row_weights(weights, row_id_map, rows: int, stream=None):
     out = torch.empty((rows,), dtype=torch.float32, device=weights.device)
     fp8q_permute_row_weights(weights, row_id_map, row_id_map.numel(), rows, out, stream)
     return out
+
+
+# ---------------------------------------------------------------- 8-bit SwiGLU checkpoints
+def fp8q_swiglu_quant_stash(gate, up, row_weights, rows: int, cols: int, q, sf, qt, sft, gq, gsf, uq, usf,
+                            stream=None) -> None:
+    import torch
+    bf16, u8, n, t = torch.bfloat16, torch.uint8, rows * cols, rows * (cols // 128)
+    _check(lib().fp8q_swiglu_quant_stash(
+        _in(gate, "gate", bf16, n), _in(up, "up", bf16, n), _in(row_weights, "row_weights", torch.float32, rows), rows,
+        cols, _in(q, "q", u8, n), _in(sf, "sf", u8, t), _in(qt, "qt", u8, n), _in(sft, "sft", u8, t),
+        _in(gq, "gq", u8, n), _in(gsf, "gsf", u8, t), _in(uq, "uq", u8, n), _in(usf, "usf", u8, t), _stream(stream)),
+        "fp8q_swiglu_quant_stash")
+
+
+def _bwd_in(gq, gsf, uq, usf, row_weights, dy, rows, cols):
+    import torch
+    u8, n, t = torch.uint8, rows * cols, rows * (cols // 128)
+    return (_in(gq, "gq", u8, n), _in(gsf, "gsf", u8, t), _in(uq, "uq", u8, n), _in(usf, "usf", u8, t),
+            _in(row_weights, "row_weights", torch.float32, rows), _in(dy, "dy", torch.bfloat16, n))
+
+
+def fp8q_swiglu_bwd(gq, gsf, uq, usf, row_weights, dy, rows: int, cols: int, dgate, dup, drow_weights,
+                    stream=None) -> None:
+    import torch
+    bf16, n = torch.bfloat16, rows * cols
+    _check(lib().fp8q_swiglu_bwd(
+        *_bwd_in(gq, gsf, uq, usf, row_weights, dy, rows, cols), rows, cols, _in(dgate, "dgate", bf16, n),
+        _in(dup, "dup", bf16, n), _in(drow_weights, "drow_weights", torch.float32, rows), _stream(stream)),
+        "fp8q_swiglu_bwd")
+
+
+def fp8q_swiglu_bwd_quant(gq, gsf, uq, usf, row_weights, dy, rows: int, cols: int, dgq, dgsf, duq, dusf, yq, ysf,
+                          drow_weights, stream=None) -> None:
+    import torch
+    u8, n, t = torch.uint8, rows * cols, rows * (cols // 128)
+    _check(lib().fp8q_swiglu_bwd_quant(
+        *_bwd_in(gq, gsf, uq, usf, row_weights, dy, rows, cols), rows, cols, _in(dgq, "dgq", u8, n),
+        _in(dgsf, "dgsf", u8, t), _in(duq, "duq", u8, n), _in(dusf, "dusf", u8, t), _in(yq, "yq", u8, n),
+        _in(ysf, "ysf", u8, t), _in(drow_weights, "drow_weights", torch.float32, rows), _stream(stream)),
+        "fp8q_swiglu_bwd_quant")
+
+
+def _pair(shape, like):
+    """Codes [rows, cols] and scales [rows, cols/128] of a row-wise pair."""
+    import torch
+    rows, cols = shape
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=like.device),
+            torch.empty((rows, cols // 128), dtype=torch.uint8, device=like.device))
+
+
+def swiglu_quant_stash(gate, up, row_weights=None, stream=None):
+    """y = silu(gate) * up (* row_weights) as a row-wise pair, and gate and up as row-wise
+    pairs for swiglu_bwd: (q, sf, gq, gsf, uq, usf)."""
+    rows, cols = gate.shape
+    _shape(up, "up", (rows, cols))
+    _shape(row_weights, "row_weights", (rows,))
+    q, sf = _pair((rows, cols), gate)
+    gq, gsf = _pair((rows, cols), gate)
+    uq, usf = _pair((rows, cols), gate)
+    fp8q_swiglu_quant_stash(gate, up, row_weights, rows, cols, q, sf, None, None, gq, gsf, uq, usf, stream)
+    return q, sf, gq, gsf, uq, usf
+
+
+def _bwd_shapes(gq, gsf, uq, usf, dy, row_weights):
+    rows, cols = gq.shape
+    for t, name in ((uq, "uq"), (dy, "dy")):
+        _shape(t, name, (rows, cols))
+    for t, name in ((gsf, "gsf"), (usf, "usf")):
+        _shape(t, name, (rows, cols // 128))
+    _shape(row_weights, "row_weights", (rows,))
+    return rows, cols
+
+
+def swiglu_bwd(gq, gsf, uq, usf, dy, row_weights=None, stream=None):
+    """Gradients of gate and up (BF16) and of the row weights (fp32, None without them) from
+    the 8-bit checkpoints and dy, the BF16 gradient of the forward's y."""
+    import torch
+    rows, cols = _bwd_shapes(gq, gsf, uq, usf, dy, row_weights)
+    dg, du = torch.empty_like(dy), torch.empty_like(dy)
+    dw = None if row_weights is None else torch.empty_like(row_weights)
+    fp8q_swiglu_bwd(gq, gsf, uq, usf, row_weights, dy, rows, cols, dg, du, dw, stream)
+    return dg, du, dw
+
+
+def swiglu_bwd_quant(gq, gsf, uq, usf, dy, row_weights=None, recompute: bool = True, stream=None):
+    """The same gradients as row-wise E4M3 pairs, with y recomputed from the checkpoints:
+    (dgq, dgsf, duq, dusf, yq, ysf, drow_weights); yq, ysf are None without `recompute`."""
+    import torch
+    rows, cols = _bwd_shapes(gq, gsf, uq, usf, dy, row_weights)
+    dgq, dgsf = _pair((rows, cols), gq)
+    duq, dusf = _pair((rows, cols), gq)
+    yq, ysf = _pair((rows, cols), gq) if recompute else (None, None)
+    dw = None if row_weights is None else torch.empty_like(row_weights)
+    fp8q_swiglu_bwd_quant(gq, gsf, uq, usf, row_weights, dy, rows, cols, dgq, dgsf, duq, dusf, yq, ysf, dw, stream)
+    return dgq, dgsf, duq, dusf, yq, ysf, dw

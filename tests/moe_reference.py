@@ -85,3 +85,55 @@ def router_units(logits):
     fin = l[np.isfinite(l) & (np.abs(l) < 1e30)]
     span = float(fin.max() - fin.min()) if fin.size else 0.0
     return span + 4 + 37 + 8
+
+
+E4M3 = np.array([(-1.0 if c >> 7 else 1.0) * (((c & 7) / 8.0) * 2.0 ** -6 if (c >> 3 & 15) == 0
+                                             else (1 + (c & 7) / 8.0) * 2.0 ** ((c >> 3 & 15) - 7)) for c in range(256)])
+
+
+def decode8(q, sf):
+    """Values of a row-wise pair (numpy uint8), float64."""
+    return E4M3[q] * np.repeat(2.0 ** (sf.astype(np.float64) - 127), 128, axis=1)
+
+
+def encode8(x):
+    """The row-wise pair of exact values x (float64 [rows, cols]): least e with amax <= 448 * 2^e
+    (0 for a zero tile, at least -127), nearest code, ties to the even one."""
+    rows, cols = x.shape
+    t = x.reshape(rows, cols // 128, 128)
+    amax = np.abs(t).max(2)
+    m, p = np.frexp(amax)
+    e = np.where(amax == 0, 0, np.maximum(p - 9 + (m > 0.875), -127))
+    v = np.abs(t) / 2.0 ** e[..., None].astype(np.float64)
+    grid = E4M3[:127]
+    hi = np.clip(np.searchsorted(grid, v), 1, 126)
+    lo = hi - 1
+    a, b = v - grid[lo], grid[hi] - v
+    code = np.where((a < b) | ((a == b) & (lo % 2 == 0)), lo, hi)
+    code = code + 128 * np.signbit(t)
+    return code.astype(np.uint8).reshape(rows, cols), (e + 127).astype(np.uint8)
+
+
+def swiglu_bwd(g, u, dy, w):
+    """(dgate, dup, y, dw) in float64 and, for each, a bound of the fp32 kernel's error.
+
+    The kernel's exp(-g) is off by 1.5 |g| + 4 half steps (the argument's rounding, the
+    hardware's exponential), s = 1 / (1 + exp(-g)) by 4 more; 1 - s adds an absolute half
+    step, so the slope s (1 + g (1 - s)) is off by that count times s (1 + |g|).  Below
+    2^-126 the hardware flushes to zero."""
+    with np.errstate(over="ignore"):
+        s = 1.0 / (1.0 + np.exp(-g))
+        q = 1.0 / (1.0 + np.exp(g))
+    w = np.ones((g.shape[0], 1)) if w is None else np.asarray(w, np.float64)[:, None]
+    act, slope = g * s, s * (1.0 + g * q)
+    n = 2 * (1.5 * np.abs(g) + 16) * U
+    tiny = 2.0 ** -125
+    n = np.minimum(n, 1.0)
+    mag = s * (1.0 + np.abs(g))
+    e_slope, e_act = mag * n + tiny * (1 + np.abs(g)), np.abs(act) * n + tiny * np.abs(g)
+    dw_terms = dy * act * u
+    cols = g.shape[1]
+    return dict(dg=w * dy * u * slope, du=w * dy * act, y=w * act * u, dw=dw_terms.sum(1),
+                e_dg=np.abs(w * dy * u) * e_slope, e_du=np.abs(w * dy) * e_act, e_y=np.abs(w * u) * e_act,
+                # the terms' errors, and the additions: 16 * ceil(cols / 4096) in a lane, 3, at most 32
+                e_dw=(np.abs(dy * u) * e_act).sum(1) + np.abs(dw_terms).sum(1) * (16 * -(-cols // 4096) + 40) * U)

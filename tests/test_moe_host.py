@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import scaling_aware_transpose_b200 as sat
-from moe_reference import router, router_bwd
+from moe_reference import router, router_bwd, swiglu_bwd
 from scaling_aware_transpose_b200 import build as lib_build
 
 A, M8, M2 = 0x10000, 0x10008, 0x10002
@@ -81,3 +81,51 @@ def test_reference_gradient_against_differences(sigmoid, renorm):
             a[t, e] += h
             b[t, e] -= h
             assert abs((value(a) - value(b)) / (2 * h) - got[t, e]) < 1e-8
+
+
+def test_swiglu_stash_refusals(L):
+    def f(g=A, u=A, w=None, rows=128, cols=256, q=A, sf=A, qt=None, sft=None, gq=A, gsf=A, uq=A, usf=A):
+        return L.fp8q_swiglu_quant_stash(g, u, w, rows, cols, q, sf, qt, sft, gq, gsf, uq, usf, None)
+
+    for kw in (dict(rows=-1), dict(cols=100), dict(rows=1 << 31), dict(rows=100, qt=A, sft=A)):
+        assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
+    for kw in (dict(qt=A), dict(sft=A)):
+        assert f(**kw) == sat.FP8Q_ERR_ARG, kw
+    for k in ("g", "u", "q", "sf", "gq", "gsf", "uq", "usf"):
+        assert f(**{k: None}) == sat.FP8Q_ERR_NULL, k
+    for kw in (dict(g=M8), dict(u=M8), dict(gq=M8), dict(uq=M8), dict(q=M8), dict(w=M2), dict(qt=M2, sft=A)):
+        assert f(**kw) == sat.FP8Q_ERR_ALIGN, kw
+    assert f(rows=0, g=None) == sat.FP8Q_OK and f(cols=0, gq=None) == sat.FP8Q_OK
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_swiglu_bwd_refusals(L, quant):
+    def f(gq=A, gsf=A, uq=A, usf=A, w=None, dy=A, rows=4, cols=256, dw=None, yq=None, ysf=None, **o):
+        dg, du, dgsf, dusf = (o.get(k, A) for k in ("dg", "du", "dgsf", "dusf"))
+        if quant:
+            return L.fp8q_swiglu_bwd_quant(gq, gsf, uq, usf, w, dy, rows, cols, dg, dgsf, du, dusf, yq, ysf, dw, None)
+        return L.fp8q_swiglu_bwd(gq, gsf, uq, usf, w, dy, rows, cols, dg, du, dw, None)
+
+    for kw in (dict(rows=-1), dict(cols=130), dict(cols=-128), dict(rows=1 << 31)):
+        assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
+    assert f(dw=A) == sat.FP8Q_ERR_ARG                       # a gradient of weights that were not given
+    for k in ("gq", "gsf", "uq", "usf", "dy", "dg", "du") + (("dgsf", "dusf") if quant else ()):
+        assert f(**{k: None}) == sat.FP8Q_ERR_NULL, k
+    for k in ("gq", "uq", "dy", "dg", "du"):
+        assert f(**{k: M8}) == sat.FP8Q_ERR_ALIGN, k
+    assert f(w=M2) == sat.FP8Q_ERR_ALIGN
+    if quant:
+        assert f(yq=A) == sat.FP8Q_ERR_ARG and f(ysf=A) == sat.FP8Q_ERR_ARG
+        assert f(yq=M8, ysf=A) == sat.FP8Q_ERR_ALIGN
+    assert f(rows=0, gq=None) == sat.FP8Q_OK
+
+
+def test_reference_swiglu_gradient_against_differences():
+    rng = np.random.default_rng(5)
+    g, u, dy, w = rng.standard_normal((3, 8)) * 3, rng.standard_normal((3, 8)), rng.standard_normal((3, 8)), rng.random(3)
+    r = swiglu_bwd(g, u, dy, w)
+    y = lambda g, u, w: g / (1 + np.exp(-g)) * u * w[:, None]  # noqa: E731
+    h = 1e-6
+    assert np.allclose((y(g + h, u, w) - y(g - h, u, w)) / (2 * h) * dy, r["dg"], atol=1e-8)
+    assert np.allclose((y(g, u + h, w) - y(g, u - h, w)) / (2 * h) * dy, r["du"], atol=1e-8)
+    assert np.allclose(((y(g, u, w + h) - y(g, u, w - h)) / (2 * h) * dy).sum(1), r["dw"], atol=1e-7)
