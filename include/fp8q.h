@@ -456,6 +456,54 @@ fp8q_status fp8q_swiglu_bwd_quant(const uint8_t *gq, const uint8_t *gsf, const u
                                   uint8_t *dgsf, uint8_t *duq, uint8_t *dusf, uint8_t *yq, uint8_t *ysf,
                                   float *drow_weights, fp8q_stream_t stream);
 
+/* ------------------------------------------------------------------ MXFP4 products
+ * Microscaled 4-bit operands (low-precision format table: MXFP4 = E2M1 elements with one
+ * power-of-two scale per 32 elements) and their products on the tensor cores.
+ *   codes  : u8 [rows, k/2]: two E2M1 codes to a byte, the even element in the low half;
+ *            E2M1 = sign, 2 exponent bits, 1 mantissa bit: magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ *            4, 6 for the codes 0..7.
+ *   scales : UE8M0 bytes, one per 1x32 tile, stored as the tensor cores read them: 512-byte
+ *            tiles of 128 rows x 4 scales, tile (r/128, c/4) for row r and scale column
+ *            c = element/32, tiles in row-major order [ceil(rows/128), k/128], and inside a
+ *            tile byte (r%32)*16 + (r%128/32)*4 + c%4.  fp8q_mxfp4_sf_bytes(rows, k) bytes,
+ *            16-byte aligned.  (scaling_aware_transpose_b200.mxfp4_tile_scales lays out the
+ *            row-major scales of a checkpoint.)
+ * k % 128 == 0 throughout.
+ *
+ * fp8q_quantize_rowwise_mxfp4: x bf16 [rows, cols] -> q u8 [rows, cols/2], sf.  Per 1x32 tile
+ *   S = 2^e with the smallest e such that amax <= 6 * 2^e (e = 0 for an all-zero tile, at
+ *   least -127), q = RNE(x / S).  The scale bytes of the rows that fill up the last 128 are
+ *   written too (127).  x, q, sf 16-byte aligned.  Errors: NULL, ALIGN, SHAPE, CUDA.
+ *
+ * fp8q_permute_pad_mxfp4: the permute of fp8q_permute_pad_quant (same arguments, routing,
+ *   padding, errors and workspace), with this quantization: q u8 [max_out_rows, hidden/2],
+ *   sf fp8q_mxfp4_sf_bytes(max_out_rows, hidden) bytes.  Padding rows hold codes 0 and scale
+ *   bytes 127; rows at or beyond expert_offsets[num_experts] are not written.
+ *
+ * fp8q_matmul_mxfp4: out = A * B^T, BF16 [m, n] rounded once from fp32 sums.
+ *   aq, asf : A [m, k];  bq, bsf : B [n, k].
+ *   group_offsets : NULL with num_groups == 1 for one product, or a DEVICE int32 array
+ *       [num_groups + 1] as fp8q_direct_transpose takes it (from 0, non-decreasing, groups
+ *       of a multiple of 128 rows: a permute with align 128; at most m, which is then the
+ *       capacity).  B is then [num_groups * n, k], group g's rows being g*n .. g*n + n - 1,
+ *       n % 128 == 0, and rows group_offsets[g] .. group_offsets[g+1] - 1 of out are
+ *       A's times group g's B.  Rows of out past the last group are not written; a group
+ *       may be empty.  Violations found on the device set FP8Q_ERR_SHAPE in the status word
+ *       and skip the offending tiles.
+ *   n is any size in the dense form.  m == 0 or n == 0 is a no-op; k == 0 is FP8Q_ERR_SHAPE.
+ *   A scale byte 255 (NaN) makes its products NaN.  Alignment 16 bytes (group_offsets 4).
+ *   Errors: NULL, ALIGN, SHAPE, ARG (num_groups), CUDA; TIMEOUT in the status word. */
+size_t fp8q_mxfp4_sf_bytes(int64_t rows, int64_t k);
+fp8q_status fp8q_quantize_rowwise_mxfp4(const void *x, int64_t rows, int64_t cols, uint8_t *q, uint8_t *sf,
+                                        fp8q_stream_t stream);
+fp8q_status fp8q_permute_pad_mxfp4(const void *x, int64_t tokens, int64_t hidden, const int32_t *topk_idx,
+                                   int32_t topk, int32_t num_experts, int32_t align, uint8_t *q, uint8_t *sf,
+                                   int64_t max_out_rows, int32_t *expert_offsets, int32_t *row_id_map,
+                                   void *workspace, size_t workspace_bytes, fp8q_stream_t stream);
+fp8q_status fp8q_matmul_mxfp4(const uint8_t *aq, const uint8_t *asf, int64_t m, const uint8_t *bq,
+                              const uint8_t *bsf, int64_t n, int64_t k, const int32_t *group_offsets,
+                              int32_t num_groups, void *out, fp8q_stream_t stream);
+
 /* Test hook for the bounded-wait machinery (no counterpart on the pages): launches one
  * CTA that waits on an mbarrier nobody arrives at, giving up after `timeout_ns`
  * nanoseconds (clamped to [1e3, 2e9]); the kernel then records FP8Q_ERR_TIMEOUT in the

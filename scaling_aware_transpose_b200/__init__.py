@@ -87,6 +87,10 @@ def lib() -> ctypes.CDLL:
             "fp8q_swiglu_quant_stash": ([P, P, P, I64, I64, P, P, P, P, P, P, P, P, P], ctypes.c_int),
             "fp8q_swiglu_bwd": ([P, P, P, P, P, P, I64, I64, P, P, P, P], ctypes.c_int),
             "fp8q_swiglu_bwd_quant": ([P, P, P, P, P, P, I64, I64, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "fp8q_mxfp4_sf_bytes": ([I64, I64], SZ),
+            "fp8q_quantize_rowwise_mxfp4": ([P, I64, I64, P, P, P], ctypes.c_int),
+            "fp8q_permute_pad_mxfp4": ([P, I64, I64, P, I32, I32, I32, P, P, I64, P, P, P, SZ, P], ctypes.c_int),
+            "fp8q_matmul_mxfp4": ([P, P, I64, P, P, I64, I64, P, I32, P, P], ctypes.c_int),
             "fp8q_permute_row_weights": ([P, P, I64, I64, P, P], ctypes.c_int),
             "fp8q_version": ([], ctypes.c_int),
         }

@@ -1,0 +1,198 @@
+// mxfp4_quant.cu — BF16 rows -> MXFP4 (see mxfp4.cuh), and the same fused with the MoE
+// permute, for the products of mxfp4_matmul.cu.
+//
+// Two lanes per 32-element tile, 16 elements (two 16-byte loads) each: a tile's amax takes
+// one shuffle, and eight lanes hold a 128-element unit whose four scale bytes leave as one
+// word of the tiled layout.  2 B are read and 0.53 B written per element: bound by HBM.
+#include "abi_checks.h"
+#include "launch.h"
+#include "mxfp4.cuh"
+#include "permute_common.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 2;  // 128-element units per eight lanes
+
+struct Unit {
+  uint2 codes;     // this lane's 16 codes
+  uint32_t scales; // the unit's four scale bytes (in every lane of the eight)
+};
+
+// Lane `sub` of eight holds elements 16 sub .. 16 sub + 15 of the unit.
+__device__ __forceinline__ Unit quantize_unit(const uint4& a, const uint4& b, int sub) {
+  uint32_t m = maxabs_bf16x2(maxabs_bf16x2(maxabs_bf16x2(a.x, a.y), maxabs_bf16x2(a.z, a.w)),
+                             maxabs_bf16x2(maxabs_bf16x2(b.x, b.y), maxabs_bf16x2(b.z, b.w)));
+  m = maxabs_bf16x2(m, __byte_perm(m, 0u, 0x1032)) & 0x7FFFu;
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const int e = mxfp4_tile_exponent(m);
+  const float s = exp2_neg(e);
+  Unit u;
+  u.codes = make_uint2(encode8_e2m1(a, s), encode8_e2m1(b, s));
+  u.scales = (uint32_t)(e + 127) << (8 * (sub >> 1));
+  u.scales |= __shfl_xor_sync(0xFFFFFFFFu, u.scales, 2);
+  u.scales |= __shfl_xor_sync(0xFFFFFFFFu, u.scales, 4);
+  return u;
+}
+
+// Rows up to the next multiple of 128 get scale bytes (127) and no codes.
+__global__ void __launch_bounds__(kThreads) quantize_mxfp4_kernel(const uint4* __restrict__ x, int64_t rows,
+                                                                  int k128, int64_t n_units, uint2* __restrict__ q,
+                                                                  uint8_t* __restrict__ sf) {
+  pdl_wait_for(x);
+  pdl_trigger();
+  const int sub = threadIdx.x & 7;
+  const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 8);
+  uint4 a[kUnits], b[kUnits];
+  const int64_t live = rows * k128;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * step;
+    a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (u < live) {
+      a[i] = ld_stream(x + u * 16 + 2 * sub);
+      b[i] = ld_stream(x + u * 16 + 2 * sub + 1);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * step;
+    const Unit v = quantize_unit(a[i], b[i], sub);
+    if (u < live) q[u * 8 + sub] = v.codes;
+    if (u < n_units && sub == 0) {
+      const int64_t r = u / k128;
+      *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, u - r * k128, k128)) = v.scales;
+    }
+  }
+}
+
+// The permute's payload: each unit is quantized once and written to the token's top-k
+// destination rows; the trailing CTAs fill the padding rows (codes 0, scale bytes 127).
+__global__ void __launch_bounds__(kThreads) scatter_mxfp4_kernel(const uint4* __restrict__ x, int64_t tokens, int k128,
+                                                                 const int32_t* __restrict__ row_id_map, int topk,
+                                                                 uint2* __restrict__ q, uint8_t* __restrict__ sf,
+                                                                 int64_t scatter_ctas, int pad_slots,
+                                                                 const int32_t* __restrict__ offsets,
+                                                                 const int32_t* __restrict__ totals,
+                                                                 int64_t max_rows) {
+  if ((int64_t)blockIdx.x >= scatter_ctas) {
+    pdl_wait_for(offsets, totals);
+    const int64_t c = (int64_t)blockIdx.x - scatter_ctas;
+    const int e = (int)(c / pad_slots);
+    const int64_t start = (int64_t)offsets[e] + totals[e] + (c - (int64_t)e * pad_slots) * kPadRowsPerCta;
+    const int64_t end = min(min(start + kPadRowsPerCta, (int64_t)offsets[e + 1]), max_rows);
+    if (start < 0 || start >= end) return;
+    for (int64_t i = threadIdx.x; i < (end - start) * k128 * 8; i += kThreads) q[start * k128 * 8 + i] = make_uint2(0u, 0u);
+    for (int64_t i = threadIdx.x; i < (end - start) * k128; i += kThreads) {
+      const int64_t r = i / k128;
+      *reinterpret_cast<uint32_t*>(sf + sf_word_offset(start + r, i - r * k128, k128)) = 0x7F7F7F7Fu;
+    }
+    return;
+  }
+  const int sub = threadIdx.x & 7;
+  const int64_t n_units = tokens * k128;
+  const int64_t first = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * (4 * kUnits) + ((threadIdx.x & 31) >> 3);
+  uint4 a[kUnits], b[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + 4 * i;
+    a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (u < n_units) {
+      a[i] = ld_stream(x + u * 16 + 2 * sub);
+      b[i] = ld_stream(x + u * 16 + 2 * sub + 1);
+    }
+  }
+  Unit v[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) v[i] = quantize_unit(a[i], b[i], sub);
+  pdl_wait_for(row_id_map);  // the row ids: everything above overlaps the routing
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + 4 * i;
+    if (u >= n_units) continue;
+    const int64_t t = u / k128, c4 = u - t * k128;
+    for (int k = 0; k < topk; ++k) {
+      const int64_t r = ld_g(row_id_map + t * topk + k);
+      if (r < 0 || r >= max_rows) continue;  // (never out of range for a consistent routing)
+      q[(r * k128 + c4) * 8 + sub] = v[i].codes;
+      if (sub == 0) *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, c4, k128)) = v[i].scales;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" {
+
+size_t fp8q_mxfp4_sf_bytes(int64_t rows, int64_t k) {
+  if (rows <= 0 || k <= 0) return 0;
+  return (size_t)((rows + 127) / 128) * (size_t)((k + 127) / 128) * kSfTileBytes;
+}
+
+fp8q_status fp8q_quantize_rowwise_mxfp4(const void* x, int64_t rows, int64_t cols, uint8_t* q, uint8_t* sf,
+                                        fp8q_stream_t stream) {
+  if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxInt32 || cols > kMaxInt32) return FP8Q_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  if (!x || !q || !sf) return FP8Q_ERR_NULL;
+  if (!aligned_to(x, 16) || !aligned_to(q, 16) || !aligned_to(sf, 16)) return FP8Q_ERR_ALIGN;
+  const int k128 = (int)(cols / 128);
+  const int64_t n_units = (rows + 127) / 128 * 128 * k128;
+  const int64_t ctas = (n_units + kUnits * (kThreads / 8) - 1) / (kUnits * (kThreads / 8));
+  if (ctas > kMaxInt32) return FP8Q_ERR_SHAPE;
+  return launch_after(quantize_mxfp4_kernel, dim3((unsigned)ctas), kThreads, 0, to_stream(stream),
+                      static_cast<const uint4*>(x), rows, k128, n_units, reinterpret_cast<uint2*>(q), sf) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
+}
+
+fp8q_status fp8q_permute_pad_mxfp4(const void* x, int64_t tokens, int64_t hidden, const int32_t* topk_idx,
+                                   int32_t topk, int32_t num_experts, int32_t align, uint8_t* q, uint8_t* sf,
+                                   int64_t max_out_rows, int32_t* expert_offsets, int32_t* row_id_map, void* workspace,
+                                   size_t workspace_bytes, fp8q_stream_t stream) {
+  if (tokens < 0 || hidden < 0 || hidden % 128 || hidden > kMaxInt32) return FP8Q_ERR_SHAPE;
+  if (topk < 1 || topk > 64 || num_experts < 1 || num_experts > kMaxExperts || align < 1 || align > 4096)
+    return FP8Q_ERR_ARG;
+  if (tokens > kMaxInt32 / topk) return FP8Q_ERR_SHAPE;
+  if (max_out_rows < tokens * topk + (int64_t)num_experts * (align - 1) || max_out_rows > kMaxInt32) return FP8Q_ERR_ARG;
+  if (!expert_offsets) return FP8Q_ERR_NULL;
+  if (!aligned_to(expert_offsets, 4)) return FP8Q_ERR_ALIGN;
+  cudaStream_t st = to_stream(stream);
+  if (tokens > 0) {
+    if (!topk_idx || !row_id_map || !workspace) return FP8Q_ERR_NULL;
+    if (!aligned_to(workspace, 16) || !aligned_to(topk_idx, 4) || !aligned_to(row_id_map, 4)) return FP8Q_ERR_ALIGN;
+    if (workspace_bytes < fp8q_permute_workspace_bytes(tokens, topk, num_experts)) return FP8Q_ERR_ARG;
+    if (hidden > 0) {
+      if (!x || !q || !sf) return FP8Q_ERR_NULL;
+      if (!aligned_to(x, 16) || !aligned_to(q, 16) || !aligned_to(sf, 16)) return FP8Q_ERR_ALIGN;
+    }
+  }
+  DeviceInfo dev;
+  if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
+  if (tokens == 0)
+    return cudaMemsetAsync(expert_offsets, 0, (size_t)(num_experts + 1) * sizeof(int32_t), st) == cudaSuccess
+               ? FP8Q_OK
+               : FP8Q_ERR_CUDA;
+  const int k128 = (int)(hidden / 128);
+  const int64_t n_units = tokens * k128;
+  const int64_t per = (kThreads / 32) * 4 * kUnits;
+  const int64_t scatter_ctas = (n_units + per - 1) / per;
+  const int pad_slots = (align - 1 + kPadRowsPerCta - 1) / kPadRowsPerCta;  // 0 when align == 1
+  const int64_t ctas = scatter_ctas + (int64_t)num_experts * pad_slots;
+  if (ctas > kMaxInt32) return FP8Q_ERR_SHAPE;
+  const fp8q_status rs =
+      route_pairs(dev, tokens, topk_idx, topk, num_experts, align, false, expert_offsets, row_id_map, workspace, st);
+  if (rs != FP8Q_OK || hidden == 0) return rs;
+  const int32_t* totals = route_totals(workspace, tokens, topk, num_experts);
+  return launch_after(scatter_mxfp4_kernel, dim3((unsigned)ctas), kThreads, 0, st, static_cast<const uint4*>(x), tokens,
+                      k128, (const int32_t*)row_id_map, (int)topk, reinterpret_cast<uint2*>(q), sf, scatter_ctas,
+                      pad_slots, (const int32_t*)expert_offsets, totals, max_out_rows) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -8,13 +8,15 @@ tensor (device, type, contiguity, size) before the library sees its address.
 """
 from __future__ import annotations
 
-from . import _check, _stream, lib
+from . import _check, _stream, fp8q_permute_workspace_bytes, lib, permute_max_rows
 
 __all__ = [
     "ROUTER_SIGMOID", "ROUTER_RENORM", "ROUTER_BF16", "fp8q_router_workspace_bytes", "fp8q_router_topk",
     "fp8q_router_topk_bwd", "fp8q_permute_row_weights", "router_topk", "router_topk_bwd", "permute_row_weights",
     "fp8q_swiglu_quant_stash", "fp8q_swiglu_bwd", "fp8q_swiglu_bwd_quant", "swiglu_quant_stash", "swiglu_bwd",
     "swiglu_bwd_quant",
+    "fp8q_mxfp4_sf_bytes", "fp8q_quantize_rowwise_mxfp4", "fp8q_permute_pad_mxfp4", "fp8q_matmul_mxfp4",
+    "mxfp4_tile_scales", "quantize_rowwise_mxfp4", "permute_pad_mxfp4", "matmul_mxfp4",
 ]
 
 ROUTER_SIGMOID = 0x1  # FP8Q_ROUTER_SIGMOID
@@ -256,3 +258,101 @@ def swiglu_bwd_quant(gq, gsf, uq, usf, dy, row_weights=None, recompute: bool = T
     dw = None if row_weights is None else torch.empty_like(row_weights)
     fp8q_swiglu_bwd_quant(gq, gsf, uq, usf, row_weights, dy, rows, cols, dgq, dgsf, duq, dusf, yq, ysf, dw, stream)
     return dgq, dgsf, duq, dusf, yq, ysf, dw
+
+
+# ---------------------------------------------------------------- MXFP4
+def fp8q_mxfp4_sf_bytes(rows: int, k: int) -> int:
+    return int(lib().fp8q_mxfp4_sf_bytes(rows, k))
+
+
+def fp8q_quantize_rowwise_mxfp4(x, rows: int, cols: int, q, sf, stream=None) -> None:
+    import torch
+    u8 = torch.uint8
+    _check(lib().fp8q_quantize_rowwise_mxfp4(
+        _in(x, "x", torch.bfloat16, rows * cols), rows, cols, _in(q, "q", u8, rows * (cols // 2)),
+        _in(sf, "sf", u8, fp8q_mxfp4_sf_bytes(rows, cols)), _stream(stream)), "fp8q_quantize_rowwise_mxfp4")
+
+
+def fp8q_permute_pad_mxfp4(x, tokens: int, hidden: int, topk_idx, topk: int, num_experts: int, align: int, q, sf,
+                           max_out_rows: int, expert_offsets, row_id_map, workspace, workspace_bytes: int,
+                           stream=None) -> None:
+    import torch
+    u8, i32 = torch.uint8, torch.int32
+    _check(lib().fp8q_permute_pad_mxfp4(
+        _in(x, "x", torch.bfloat16, tokens * hidden), tokens, hidden, _in(topk_idx, "topk_idx", i32, tokens * topk),
+        topk, num_experts, align, _in(q, "q", u8, max_out_rows * (hidden // 2)),
+        _in(sf, "sf", u8, fp8q_mxfp4_sf_bytes(max_out_rows, hidden)), max_out_rows,
+        _in(expert_offsets, "expert_offsets", i32, num_experts + 1), _in(row_id_map, "row_id_map", i32, tokens * topk),
+        _in(workspace, "workspace", u8, workspace_bytes), workspace_bytes, _stream(stream)), "fp8q_permute_pad_mxfp4")
+
+
+def fp8q_matmul_mxfp4(aq, asf, m: int, bq, bsf, n: int, k: int, group_offsets, num_groups: int, out,
+                      stream=None) -> None:
+    import torch
+    u8, b_rows = torch.uint8, n * num_groups
+    _check(lib().fp8q_matmul_mxfp4(
+        _in(aq, "aq", u8, m * (k // 2)), _in(asf, "asf", u8, fp8q_mxfp4_sf_bytes(m, k)), m,
+        _in(bq, "bq", u8, b_rows * (k // 2)), _in(bsf, "bsf", u8, fp8q_mxfp4_sf_bytes(b_rows, k)), n, k,
+        _in(group_offsets, "group_offsets", torch.int32, num_groups + 1), num_groups,
+        _in(out, "out", torch.bfloat16, m * n), _stream(stream)), "fp8q_matmul_mxfp4")
+
+
+def mxfp4_tile_scales(sf):
+    """Row-major scale bytes u8 [rows, k/32] (k % 128 == 0), as a checkpoint holds them -> the
+    tiled order of the products (flat, fp8q_mxfp4_sf_bytes(rows, k) bytes; rows that fill up
+    the last 128 get 127).  A layout step for weights, done once when they are loaded."""
+    import torch
+    rows, c = sf.shape
+    if sf.dtype != torch.uint8 or c % 4:
+        raise ValueError("scale bytes: uint8 [rows, k/32] with k a multiple of 128")
+    blocks = (rows + 127) // 128
+    full = torch.full((blocks * 128, c), 127, dtype=torch.uint8, device=sf.device)
+    full[:rows] = sf
+    return full.view(blocks, 4, 32, c // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+
+
+def quantize_rowwise_mxfp4(x, stream=None):
+    """x: bf16 [rows, cols] -> (q u8 [rows, cols/2], sf u8 flat, in the products' order)."""
+    import torch
+    rows, cols = x.shape
+    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+    sf = torch.empty((fp8q_mxfp4_sf_bytes(rows, cols),), dtype=torch.uint8, device=x.device)
+    fp8q_quantize_rowwise_mxfp4(x, rows, cols, q, sf, stream)
+    return q, sf
+
+
+def permute_pad_mxfp4(x, topk_idx, num_experts: int, align: int, max_out_rows: int | None = None, stream=None):
+    """permute_pad_quant with 4-bit rows: (q u8 [max_out_rows, hidden/2], sf, expert_offsets
+    [E+1], row_id_map [T*K])."""
+    import torch
+    tokens, hidden = x.shape
+    topk = topk_idx.shape[1]
+    _shape(topk_idx, "topk_idx", (tokens, topk))
+    if max_out_rows is None:
+        max_out_rows = permute_max_rows(tokens, topk, num_experts, align)
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
+    q = new((max_out_rows, hidden // 2), torch.uint8)
+    sf = new((fp8q_mxfp4_sf_bytes(max_out_rows, hidden),), torch.uint8)
+    off, rmap = new((num_experts + 1,), torch.int32), new((tokens * topk,), torch.int32)
+    ws = _scratch(fp8q_permute_workspace_bytes(tokens, topk, num_experts), x, stream)
+    fp8q_permute_pad_mxfp4(x, tokens, hidden, topk_idx, topk, num_experts, align, q, sf, max_out_rows, off, rmap, ws,
+                           ws.numel(), stream)
+    return q, sf, off, rmap
+
+
+def matmul_mxfp4(aq, asf, bq, bsf, group_offsets=None, out=None, stream=None):
+    """BF16 [m, n] = A [m, k] times B [n, k] transposed, both MXFP4 (codes [rows, k/2], scales in
+    the products' order).  With group_offsets (device int32 [G+1], as the permutes write them
+    with align 128) bq is [G*n, k/2]: rows of group g are multiplied by its n rows; rows of
+    out past the last group are not written (pass `out` to say what they hold)."""
+    import torch
+    m, k = aq.shape[0], 2 * aq.shape[1]
+    groups = 1 if group_offsets is None else group_offsets.numel() - 1
+    if bq.shape[1] * 2 != k or groups < 1 or bq.shape[0] % groups:
+        raise ValueError(f"codes {tuple(aq.shape)} and {tuple(bq.shape)} do not fit ({groups} groups)")
+    n = bq.shape[0] // groups
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=aq.device)
+    _shape(out, "out", (m, n))
+    fp8q_matmul_mxfp4(aq, asf, m, bq, bsf, n, k, group_offsets, groups, out, stream)
+    return out

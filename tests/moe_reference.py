@@ -137,3 +137,47 @@ def swiglu_bwd(g, u, dy, w):
                 e_dg=np.abs(w * dy * u) * e_slope, e_du=np.abs(w * dy) * e_act, e_y=np.abs(w * u) * e_act,
                 # the terms' errors, and the additions: 16 * ceil(cols / 4096) in a lane, 3, at most 32
                 e_dw=(np.abs(dy * u) * e_act).sum(1) + np.abs(dw_terms).sum(1) * (16 * -(-cols // 4096) + 40) * U)
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0])
+
+
+def encode4(x):
+    """(codes u8 [rows, cols/2], scale bytes u8 [rows, cols/32] row-major) of exact values x."""
+    rows, cols = x.shape
+    t = np.asarray(x, np.float64).reshape(rows, cols // 32, 32)
+    amax = np.abs(t).max(2)
+    m, p = np.frexp(amax)
+    e = np.where(amax == 0, 0, np.maximum(p - 3 + (m > 0.75), -127))
+    v = np.abs(t) / 2.0 ** e[..., None].astype(np.float64)
+    grid = E2M1[:8]
+    hi = np.clip(np.searchsorted(grid, v), 1, 7)
+    lo = hi - 1
+    a, b = v - grid[lo], grid[hi] - v
+    code = np.where((a < b) | ((a == b) & (lo % 2 == 0)), lo, hi) + 8 * np.signbit(t)
+    code = code.astype(np.uint8).reshape(rows, cols // 2, 2)
+    return code[..., 0] | (code[..., 1] << 4), (e + 127).astype(np.uint8)
+
+
+def decode4(q, sf):
+    rows, half = q.shape
+    v = np.stack([E2M1[q & 15], E2M1[q >> 4]], 2).reshape(rows, 2 * half)
+    return v * np.repeat(2.0 ** (sf.astype(np.float64) - 127), 32, axis=1)
+
+
+def tile_scales(sf, fill=127):
+    """Row-major scale bytes -> the products' order, one byte at a time by its definition."""
+    rows, c = sf.shape
+    out = np.full(((rows + 127) // 128) * (c // 4) * 512, fill, np.uint8)
+    r, k = np.meshgrid(np.arange(rows), np.arange(c), indexing="ij")
+    out[((r // 128) * (c // 4) + k // 4) * 512 + (r % 32) * 16 + (r % 128 // 32) * 4 + k % 4] = sf
+    return out
+
+
+def matmul_bound(a, b):
+    """Error bound of an fp32 tensor-core product rounded to BF16: each MMA of 64 elements
+    adds to the accumulator with at most 2^-22 of the magnitudes summed so far, then half a
+    BF16 step."""
+    k = a.shape[1]
+    want = a @ b.T
+    return want, (k / 64 + 1) * 2.0 ** -22 * (np.abs(a) @ np.abs(b).T) + np.abs(want) * U_BF16 * 1.01 + 1e-37

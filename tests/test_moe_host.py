@@ -129,3 +129,67 @@ def test_reference_swiglu_gradient_against_differences():
     assert np.allclose((y(g + h, u, w) - y(g - h, u, w)) / (2 * h) * dy, r["dg"], atol=1e-8)
     assert np.allclose((y(g, u + h, w) - y(g, u - h, w)) / (2 * h) * dy, r["du"], atol=1e-8)
     assert np.allclose(((y(g, u, w + h) - y(g, u, w - h)) / (2 * h) * dy).sum(1), r["dw"], atol=1e-7)
+
+
+def test_mxfp4_quantize_refusals(L):
+    f = L.fp8q_quantize_rowwise_mxfp4
+    assert f(A, 4, 96, A, A, None) == sat.FP8Q_ERR_SHAPE
+    assert f(A, -1, 128, A, A, None) == sat.FP8Q_ERR_SHAPE
+    assert f(None, 4, 128, A, A, None) == sat.FP8Q_ERR_NULL
+    assert f(A, 4, 128, A, None, None) == sat.FP8Q_ERR_NULL
+    assert f(M8, 4, 128, A, A, None) == sat.FP8Q_ERR_ALIGN
+    assert f(A, 4, 128, A, M8, None) == sat.FP8Q_ERR_ALIGN
+    assert f(None, 0, 128, None, None, None) == sat.FP8Q_OK
+    assert sat.fp8q_mxfp4_sf_bytes(1, 128) == 512 and sat.fp8q_mxfp4_sf_bytes(129, 384) == 2 * 3 * 512
+    assert sat.fp8q_mxfp4_sf_bytes(0, 128) == 0
+
+
+def test_mxfp4_permute_refusals(L):
+    def f(x=A, T=8, H=256, idx=A, K=2, E=4, align=128, q=A, sf=A, cap=1 << 20, off=A, rmap=A, ws=A, n=1 << 30):
+        return L.fp8q_permute_pad_mxfp4(x, T, H, idx, K, E, align, q, sf, cap, off, rmap, ws, n, None)
+
+    for kw in (dict(T=-1), dict(H=100), dict(T=1 << 40)):
+        assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
+    for kw in (dict(K=0), dict(K=65), dict(E=0), dict(E=5000), dict(align=0), dict(cap=100), dict(n=4)):
+        assert f(**kw) == sat.FP8Q_ERR_ARG, kw
+    for k in ("x", "idx", "q", "sf", "off", "rmap", "ws"):
+        assert f(**{k: None}) == sat.FP8Q_ERR_NULL, k
+    for k in ("x", "q", "sf", "ws"):
+        assert f(**{k: M8}) == sat.FP8Q_ERR_ALIGN, k
+    for k in ("idx", "off", "rmap"):
+        assert f(**{k: M2}) == sat.FP8Q_ERR_ALIGN, k
+
+
+def test_mxfp4_matmul_refusals(L):
+    def f(aq=A, asf=A, m=4, bq=A, bsf=A, n=128, k=256, off=None, G=1, out=A):
+        return L.fp8q_matmul_mxfp4(aq, asf, m, bq, bsf, n, k, off, G, out, None)
+
+    for kw in (dict(m=-1), dict(n=-1), dict(k=100), dict(k=0), dict(m=1 << 31), dict(off=A, n=100),
+               dict(off=A, n=1 << 24, G=200)):
+        assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
+    for kw in (dict(G=0), dict(G=2), dict(off=A, G=0)):
+        assert f(**kw) == sat.FP8Q_ERR_ARG, kw
+    for k in ("aq", "asf", "bq", "bsf", "out"):
+        assert f(**{k: None}) == sat.FP8Q_ERR_NULL, k
+        assert f(**{k: M8}) == sat.FP8Q_ERR_ALIGN, k
+    assert f(off=M2) == sat.FP8Q_ERR_ALIGN
+    assert f(m=0, aq=None) == sat.FP8Q_OK and f(n=0, out=None) == sat.FP8Q_OK
+
+
+def test_reference_codes_round_trip():
+    from moe_reference import E4M3, decode4, decode8, encode4, encode8, tile_scales
+    rng = np.random.default_rng(1)
+    q = rng.integers(0, 256, (5, 64), dtype=np.uint8)
+    q[:, ::16] = 0x77  # the largest code in every tile: the scale is then the rule's own
+    sf = rng.integers(60, 180, (5, 4)).astype(np.uint8)
+    rq, rsf = encode4(decode4(q, sf))
+    assert np.array_equal(rq, q) and np.array_equal(rsf, sf)
+    c = rng.integers(0, 126, (3, 256), dtype=np.uint8)
+    c[:, ::128] = 126
+    s8 = rng.integers(60, 180, (3, 2)).astype(np.uint8)
+    r8, rs8 = encode8(decode8(c, s8))
+    assert np.array_equal(r8, c) and np.array_equal(rs8, s8) and E4M3[126] == 448
+    assert sorted(tile_scales(np.arange(128 * 4, dtype=np.uint32).reshape(128, 4) % 251)) == sorted(np.arange(512) % 251)
+    import torch
+    t = torch.from_numpy(rng.integers(0, 255, (200, 12), dtype=np.uint8))
+    assert np.array_equal(sat.mxfp4_tile_scales(t).numpy(), tile_scales(t.numpy()))
