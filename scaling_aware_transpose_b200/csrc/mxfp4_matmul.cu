@@ -8,21 +8,24 @@
 //
 // One persistent CTA per SM walks output tiles of 128 rows x BN columns; a pipeline stage
 // is 256 elements of k (128-byte rows under the 128-byte swizzle):
-//   warp 0   TMA loads of the A and B codes, and bulk copies of their scale tiles, which
-//            the quantizers store in the order the tensor core reads;
-//   warp 1   per stage: scales shared -> tensor memory (tcgen05.cp), four MMAs of 64
-//            elements, and a commit that frees the stage;
-//   warps 2-5  the epilogue: tensor memory -> registers -> BF16 -> global.
-// The accumulator is double-buffered in tensor memory, so the epilogue of one tile runs
-// under the MMAs of the next.  Scale columns in tensor memory belong to the stage, which
-// is refilled only after its MMAs have completed.
+//   warp 0     TMA loads of the A and B codes; every fourth stage, bulk copies of the scale
+//              tiles, which the quantizers store in the order the tensor core reads;
+//   warp 1     four MMAs of 64 elements per stage and a commit that frees it;
+//   warps 2-5  scales: shared memory -> registers -> tensor memory, each warp its quarter of
+//              the lanes.  (tcgen05.cp from the MMA thread took turns with the MMAs: 36 ns a
+//              512-byte tile, and as much again for each change from one to the other.)
+//   warps 6-9  the epilogue: tensor memory -> registers -> BF16 -> global.
+// Scale columns in tensor memory belong to the stage: they are rewritten only after the
+// stage's MMAs have completed.
 //
 // Every wait is bounded; a role whose wait expires records FP8Q_ERR_TIMEOUT and leaves its
 // loop, the others follow, outstanding copies and MMAs are waited for (again bounded) and
 // the tensor memory is freed.
 #include <cuda.h>
 
+#include <atomic>
 #include <mutex>
+
 
 #include "abi_checks.h"
 #include "launch.h"
@@ -34,25 +37,26 @@ namespace {
 constexpr int kBM = 128;
 constexpr int kBK = 256;          // elements of k per stage
 constexpr int kRowBytes = kBK / 2;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
+constexpr int kSfSteps = 4;       // stages per slot of scale tiles
+constexpr int kSfSlots = 2;
 constexpr int kTmemCols = 512;
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int ACC>
 struct Cfg {
   static constexpr int kAtoms = BN > 128 ? BN / 128 : 1;  // 128-row scale tiles per B tile
   static constexpr int kABytes = kBM * kRowBytes;
   static constexpr int kBBytes = BN * kRowBytes;
-  static constexpr int kSfaBytes = 2 * kSfTileBytes;
-  static constexpr int kSfbBytes = kAtoms * 2 * kSfTileBytes;
   // Codes first: A and B tiles stay on 1024-byte boundaries (the swizzle's period).
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kSfBytes = kSfaBytes + kSfbBytes;
-  static constexpr int kSmem = 1024 + STAGES * (kStageBytes + kSfBytes);
+  static constexpr int kSfRun = kSfSteps * 2 * kSfTileBytes;  // one 128-row tile column of a slot
+  static constexpr int kSlotBytes = (1 + kAtoms) * kSfRun;
+  static constexpr int kSmem = 1024 + STAGES * kStageBytes + kSfSlots * kSlotBytes;
   static constexpr int kSfaCols = 8, kSfbCols = 8 * kAtoms;
   static constexpr int kSfCols = kSfaCols + kSfbCols;
-  static constexpr int kAcc = 2;
+  static constexpr int kAcc = ACC;  // accumulators in tensor memory
   static_assert(kAcc * BN + STAGES * kSfCols <= kTmemCols, "tensor memory");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kSmem <= 222 * 1024, "shared memory");  // 5 KB more are static
 };
 
 struct MatmulArgs {
@@ -61,10 +65,20 @@ struct MatmulArgs {
   uint16_t* out;
   int64_t m, n;            // m: rows (dense) or the capacity (grouped)
   int k, groups;
+  int a_rows;              // rows of A that a stage loads (the rest of its 128 are never stored)
   int* status;
 };
 
 // ------------------------------------------------------------------ PTX
+// One lane of a converged warp, always the same.  The issuing roles run their loops with the
+// whole warp and put only the asynchronous instructions under it: the compiler then keeps
+// their operands in uniform registers (a loop run by one lane alone spent about 50 ns per
+// MMA moving them there).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
@@ -86,9 +100,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void tc_copy_sf(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void tc_store4(uint32_t tmem, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tmem), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
 }
+__device__ __forceinline__ void tc_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -118,14 +135,34 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// Shared-memory matrix descriptors (K-major, version 1): codes under the 128-byte swizzle,
-// eight rows of 128 bytes apart by 1024; scale tiles without swizzle, eight 16-byte rows
-// apart by 128.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// Shared-memory matrix descriptor (K-major, version 1): codes under the 128-byte swizzle,
+// eight rows of 128 bytes apart by 1024.
 __device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (8ull << 32) | (1ull << 46);
 }
 // Instruction descriptor of kind::mxf4: E2M1 operands, UE8M0 scales, M = 128, K = 64; the
 // scale ids (bits 4-5 of B, 29-30 of A) pick the half of each 4-byte scale word.
@@ -156,26 +193,33 @@ __device__ __forceinline__ bool locate(const MatmulArgs& a, int64_t t, int64_t n
   return b <= o.row && o.row < e && e <= a.m && ((b | e) & 127) == 0;
 }
 
+// Called by a whole warp; the same answer in every lane.
 __device__ __forceinline__ bool wait_or_record(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_wait_bounded(bar, parity, kWaitTimeoutNs)) return true;
+  if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, kWaitTimeoutNs))) return true;
   record_status(status, FP8Q_ERR_TIMEOUT);
   return false;
 }
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int ACC, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         MatmulArgs a) {
-  using C = Cfg<BN, STAGES>;
+  using C = Cfg<BN, STAGES, ACC>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[C::kAcc], acc_empty[C::kAcc], drain;
-  __shared__ uint32_t tmem_sh;
+  __shared__ uint64_t full[STAGES], empty[STAGES], scaled[STAGES], sf_full[kSfSlots], sf_empty[kSfSlots];
+  __shared__ uint64_t acc_full[C::kAcc], acc_empty[C::kAcc], drain;
+  __shared__ uint32_t tmem_sh, odd_rows[4][32 * 9];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&scaled[s], 4);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_empty[s], 4);
     }
     for (int s = 0; s < C::kAcc; ++s) {
       mbar_init(&acc_full[s], 1);
@@ -206,154 +250,301 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int64_t tiles = (rows + kBM - 1) / kBM * n_tiles;
   const int k128 = a.k / 128;
-  const int steps = (a.k + kBK - 1) / kBK;
+  // Persistent: tiles blockIdx.x, + gridDim.x, ..., every step of k.  Split: the CTAs of a
+  // cluster share one tile, each a contiguous run of the steps.
+  const uint32_t split = SPLIT ? cluster_size() : 1u, rank = SPLIT ? cluster_rank() : 0u;
+  const int64_t t0 = blockIdx.x / split, stride = gridDim.x / split;
+  const int all_steps = (a.k + kBK - 1) / kBK;
+  const int j0 = (int)((int64_t)all_steps * rank / split);
+  const int steps = (int)((int64_t)all_steps * (rank + 1) / split) - j0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      asm volatile("fence.proxy.async.global;" ::: "memory");
-      int s = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        Tile o;
-        if (!locate(a, t, n_tiles, BN, o)) continue;
-        const int64_t b_rows = a.offsets ? a.n * a.groups : a.n;
-        const uint8_t* sfa = a.a_sf + (o.row >> 7) * k128 * kSfTileBytes;
-        const uint8_t* sfb = a.b_sf + (o.b_row >> 7) * k128 * kSfTileBytes;
-        int atoms = 1;  // scale tiles of B that exist under this tile
-        if (C::kAtoms > 1) atoms = (int)min((int64_t)C::kAtoms, (b_rows - o.b_row + 127) >> 7);
-        for (int j = 0; j < steps; ++j) {
-          if (!wait_or_record(&empty[s], phase ^ 1u, a.status)) {
-            ok = false;
-            break;
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    int s = 0, slot = 0;
+    uint32_t phase = 0, slot_phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
+      Tile o;
+      if (!locate(a, t, n_tiles, BN, o)) continue;
+      const int64_t b_rows = a.offsets ? a.n * a.groups : a.n;
+      const uint8_t* sfa = a.a_sf + (o.row >> 7) * k128 * kSfTileBytes;
+      const uint8_t* sfb = a.b_sf + (o.b_row >> 7) * k128 * kSfTileBytes;
+      int atoms = 1;  // scale tiles of B that exist under this tile
+      if (C::kAtoms > 1) atoms = (int)min((int64_t)C::kAtoms, (b_rows - o.b_row + 127) >> 7);
+      for (int j = 0; j < steps; ++j) {
+        if (j % kSfSteps == 0) {
+          ok = wait_or_record(&sf_empty[slot], slot_phase ^ 1u, a.status);
+          if (!ok) break;
+          const uint32_t bytes = min(2 * kSfSteps, k128 - 2 * (j0 + j)) * kSfTileBytes;
+          const uint32_t sf = smem + STAGES * C::kStageBytes + slot * C::kSlotBytes;
+          if (elect_one()) {
+            mbar_expect_tx(&sf_full[slot], (1 + atoms) * bytes);
+            bulk_load(sf, sfa + (int64_t)(j0 + j) * 2 * kSfTileBytes, bytes, &sf_full[slot]);
+            for (int i = 0; i < atoms; ++i)
+              bulk_load(sf + (1 + i) * C::kSfRun, sfb + ((int64_t)i * k128 + (int64_t)(j0 + j) * 2) * kSfTileBytes, bytes,
+                        &sf_full[slot]);
           }
-          const uint32_t sf_bytes = min(2, k128 - 2 * j) * kSfTileBytes;
-          const uint32_t base = smem + s * C::kStageBytes;
-          const uint32_t sf = smem + STAGES * C::kStageBytes + s * C::kSfBytes;
-          mbar_expect_tx(&full[s], C::kStageBytes + (1 + atoms) * sf_bytes);
-          tma_load_2d(base, &map_a, j * kRowBytes, (int)o.row, &full[s]);
-          tma_load_2d(base + C::kABytes, &map_b, j * kRowBytes, (int)o.b_row, &full[s]);
-          bulk_load(sf, sfa + (int64_t)j * 2 * kSfTileBytes, sf_bytes, &full[s]);
-          for (int i = 0; i < atoms; ++i)
-            bulk_load(sf + C::kSfaBytes + i * 2 * kSfTileBytes,
-                      sfb + ((int64_t)i * k128 + (int64_t)j * 2) * kSfTileBytes, sf_bytes, &full[s]);
-          ++issued;
-          if (++s == STAGES) {
-            s = 0;
-            phase ^= 1u;
+          __syncwarp();
+          if (++slot == kSfSlots) {
+            slot = 0;
+            slot_phase ^= 1u;
           }
         }
-      }
-      // Outstanding fills end before the CTA does: on the regular path each was consumed
-      // (its stage was freed); after an expired wait its copies at least have landed.
-      for (int i = 0; i < STAGES && issued > 0; ++i, --issued) {
-        if (s == 0) {
-          s = STAGES;
+        ok = wait_or_record(&empty[s], phase ^ 1u, a.status);
+        if (!ok) break;
+        const uint32_t base = smem + s * C::kStageBytes;
+        if (elect_one()) {
+          mbar_expect_tx(&full[s], a.a_rows * kRowBytes + C::kBBytes);
+          tma_load_2d(base, &map_a, (j0 + j) * kRowBytes, (int)o.row, &full[s]);
+          tma_load_2d(base + C::kABytes, &map_b, (j0 + j) * kRowBytes, (int)o.b_row, &full[s]);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == STAGES) {
+          s = 0;
           phase ^= 1u;
         }
-        --s;
-        mbar_wait_bounded(ok ? &empty[s] : &full[s], phase, kWaitTimeoutNs);
       }
+    }
+    // Outstanding fills end before the CTA does: on the regular path each was consumed (its
+    // stage was freed); after an expired wait its copies at least have landed.
+    for (int i = 0; i < STAGES && issued > 0; ++i, --issued) {
+      if (s == 0) {
+        s = STAGES;
+        phase ^= 1u;
+      }
+      --s;
+      mbar_wait_bounded(ok ? &empty[s] : &full[s], phase, kWaitTimeoutNs);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {  // (a slot never filled passes at once)
+      if (slot == 0) {
+        slot = kSfSlots;
+        slot_phase ^= 1u;
+      }
+      --slot;
+      mbar_wait_bounded(&sf_full[slot], slot_phase, kWaitTimeoutNs);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int s = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        Tile o;
-        if (!locate(a, t, n_tiles, BN, o)) continue;
-        ok = wait_or_record(&acc_empty[acc], acc_phase ^ 1u, a.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
-        for (int j = 0; j < steps; ++j) {
-          ok = wait_or_record(&full[s], phase, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t base = smem + s * C::kStageBytes;
-          const uint32_t sf = smem + STAGES * C::kStageBytes + s * C::kSfBytes;
-          const uint32_t tm_a = tmem + C::kAcc * BN + s * C::kSfCols;
-          const uint32_t tm_b = tm_a + C::kSfaCols;
-          const int chunks = min(2, k128 - 2 * j);  // 128 elements of k each
-          for (int c = 0; c < chunks; ++c) {
-            tc_copy_sf(tm_a + 4 * c, desc_scales(sf + c * kSfTileBytes));
-            for (int i = 0; i < C::kAtoms; ++i)
-              tc_copy_sf(tm_b + 4 * (c * C::kAtoms + i),
-                         desc_scales(sf + C::kSfaBytes + (2 * i + c) * kSfTileBytes));
-          }
-          // A B tile narrower than a scale tile starts inside it: 32 rows per column.
-          const uint32_t shift = BN < 128 ? (uint32_t)(o.b_row & 127) >> 5 : 0u;
-          for (int c = 0; c < chunks; ++c) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t off = (2 * c + h) * 32;  // 64 codes
-              tc_mma_mxf4(d, desc_codes(base + off), desc_codes(base + C::kABytes + off), idesc_mxf4(BN, 2 * h),
-                          tm_a + 4 * c, tm_b + 4 * c * C::kAtoms + shift, (uint32_t)(j + c + h > 0));
-            }
-          }
-          tc_commit(&empty[s]);
-          if (++s == STAGES) {
-            s = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        tc_commit(&acc_full[acc]);
-        if (++acc == C::kAcc) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-      }
-      if (!ok) {
-        tc_commit(&drain);
-        mbar_wait_bounded(&drain, 0u, kWaitTimeoutNs);
-      }
-    }
-    __syncwarp();
-  } else {
-    const int quad = warp & 3;  // the tensor-memory lanes this warp may read
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    const bool vec = (a.n & 7) == 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    int s = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
       Tile o;
       if (!locate(a, t, n_tiles, BN, o)) continue;
-      if (!__all_sync(0xFFFFFFFFu, wait_or_record(&acc_full[acc], acc_phase, a.status))) break;
-      tc_fence_after();
-      const int64_t r = o.row + quad * 32 + lane;
-      uint16_t* dst = a.out + r * a.n + o.col;
-      const int64_t left = a.n - o.col;  // columns of this tile that exist
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t v[32];
-        tc_load32(v, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + c);
-        tc_wait_load();
-        if (r < rows) {
-          if (vec) {
+      ok = wait_or_record(&acc_empty[acc], acc_phase ^ 1u, a.status);
+      if (!ok) break;
+      const uint32_t d = tmem + acc * BN;
+      for (int j = 0; j < steps; ++j) {
+        ok = wait_or_record(&scaled[s], phase, a.status);  // the codes have landed, too
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tm_a = tmem + C::kAcc * BN + s * C::kSfCols;
+        const uint32_t tm_b = tm_a + C::kSfaCols;
+        const uint64_t da = desc_codes(smem + s * C::kStageBytes);
+        const uint64_t db = desc_codes(smem + s * C::kStageBytes + C::kABytes);
+        if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c + 8 * i < left)
-                *reinterpret_cast<uint4*>(dst + c + 8 * i) =
-                    make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < left) dst[c + i] = (uint16_t)pack_bf16(v[i], 0u);
-          }
+          for (int h = 0; h < 4; ++h)  // 64 codes: 32 bytes, two scales of a row's four-byte word
+            if (h < 2 || 2 * (j0 + j) + 1 < k128)
+              tc_mma_mxf4(d, da + 2 * h, db + 2 * h, idesc_mxf4(BN, 2 * (h & 1)), tm_a + 4 * (h >> 1),
+                          tm_b + 4 * (h >> 1) * C::kAtoms, (uint32_t)(j + h > 0));
+          tc_commit(&empty[s]);
+          if (j + 1 == steps) tc_commit(&acc_full[acc]);
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          phase ^= 1u;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
       if (++acc == C::kAcc) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
+    if (!ok) {
+      if (elect_one()) tc_commit(&drain);
+      __syncwarp();
+      mbar_wait_bounded(&drain, 0u, kWaitTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    const int quad = warp & 3;  // the tensor-memory lanes this warp may write
+    int s = 0, slot = 0;
+    uint32_t phase = 0, slot_phase = 0;
+    bool ok = true;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
+      Tile o;
+      if (!locate(a, t, n_tiles, BN, o)) continue;
+      for (int j = 0; j < steps; ++j) {
+        const uint8_t* sf = smem_raw + (smem - smem_u32(smem_raw)) + STAGES * C::kStageBytes + slot * C::kSlotBytes +
+                            (j % kSfSteps) * 2 * kSfTileBytes + lane * 16;
+        if (j % kSfSteps == 0) ok = wait_or_record(&sf_full[slot], slot_phase, a.status);
+        if (!ok) break;
+        uint4 v[2 * (1 + C::kAtoms)];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i <= C::kAtoms; ++i)
+            v[c * (1 + C::kAtoms) + i] = *reinterpret_cast<const uint4*>(sf + i * C::kSfRun + c * kSfTileBytes);
+        if (BN < 128) {
+          // A B tile narrower than a scale tile starts inside it (32 rows per word): its first
+          // word goes to the first column, whose address stays a multiple of four.
+          const uint32_t first = (uint32_t)(o.b_row & 127) >> 5;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint4& w = v[2 * c + 1];
+            if (first & 2) w = make_uint4(w.z, w.w, w.z, w.w);
+            if (first & 1) w.x = w.y;  // (32 rows: one word)
+          }
+        }
+        // A filled stage was free before: so are its scale columns.
+        ok = wait_or_record(&full[s], phase, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + C::kAcc * BN + s * C::kSfCols;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tc_store4(tm + 4 * c, v[c * (1 + C::kAtoms)]);
+#pragma unroll
+          for (int i = 0; i < C::kAtoms; ++i)
+            tc_store4(tm + C::kSfaCols + 4 * (c * C::kAtoms + i), v[c * (1 + C::kAtoms) + 1 + i]);
+        }
+        tc_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        const bool slot_done = (j + 1) % kSfSteps == 0 || j + 1 == steps;
+        if (lane == 0) {
+          mbar_arrive(&scaled[s]);
+          if (slot_done) mbar_arrive(&sf_empty[slot]);
+        }
+        if (slot_done && ++slot == kSfSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+        if (++s == STAGES) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int quad = warp & 3;  // the tensor-memory lanes this warp may read
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const bool vec = (a.n & 7) == 0;
+    for (int64_t t = t0; t < tiles; t += stride) {
+      Tile o;
+      if (!locate(a, t, n_tiles, BN, o)) continue;
+      if (!wait_or_record(&acc_full[acc], acc_phase, a.status)) break;
+      tc_fence_after();
+      const int64_t r = o.row + quad * 32 + lane;
+      if (SPLIT) {
+        // This CTA's fp32 sums go to shared memory (the stages are all consumed), one padded
+        // row per output row; they are added up below.
+        float* part = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw))) + (quad * 32 + lane) * (BN + 4);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t v[32];
+          tc_load32(v, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + c);
+          tc_wait_load();
+          if (r < rows) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(part + c + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        break;
+      }
+      uint16_t* dst = a.out + r * a.n + o.col;
+      const int left = (int)min((int64_t)BN, a.n - o.col);  // columns of this tile that exist
+      constexpr int kPart = BN < 128 ? BN : 128;  // columns packed in registers at a time
+#pragma unroll 1
+      for (int h = 0; h < BN; h += kPart) {
+        uint32_t p[kPart / 2];
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32) {
+          uint32_t v[32];
+          tc_load32(v, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + h + c);
+          tc_wait_load();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[c / 2 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        }
+        if (h + kPart == BN) {  // read to the end: the next tile's MMAs may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[acc]);
+        }
+        if (vec) {
+          if (r < rows) {
+#pragma unroll
+            for (int c = 0; c < kPart; c += 8)
+              if (h + c < left)
+                *reinterpret_cast<uint4*>(dst + h + c) = make_uint4(p[c / 2], p[c / 2 + 1], p[c / 2 + 2], p[c / 2 + 3]);
+          }
+        } else {
+          // Rows that do not start on 16 bytes: 16 columns at a time through shared memory, so
+          // that half a warp stores 16 neighbouring elements of a row (each lane storing its
+          // own row element by element took 2.5 times as long over the whole product).
+          uint32_t* mine = odd_rows[quad] + lane * 9;
+          const uint16_t* all = reinterpret_cast<const uint16_t*>(odd_rows[quad]);
+          const int rows_here = (int)max((int64_t)0, min((int64_t)32, rows - (o.row + quad * 32)));
+          uint16_t* base = a.out + (o.row + quad * 32) * a.n + o.col + h;
+#pragma unroll
+          for (int c = 0; c < kPart; c += 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[i] = p[c / 2 + i];
+            __syncwarp();
+            const int col = c + (lane & 15);
+            if (h + col < left) {
+#pragma unroll 4
+              for (int i = lane >> 4; i < rows_here; i += 2) base[i * a.n + col] = all[i * 18 + (lane & 15)];
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (++acc == C::kAcc) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+  tc_fence_before();
+  if (SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    Tile o;
+    if (t0 < tiles && locate(a, t0, n_tiles, BN, o)) {
+      const int live = (int)min((int64_t)kBM, rows - o.row);
+      const bool vec = (a.n & 3) == 0;
+      for (int i = rank * kThreads + threadIdx.x; i < live * (BN / 4); i += split * kThreads) {
+        const int r = i / (BN / 4), c = i % (BN / 4) * 4;
+        if (o.col + c >= a.n) continue;
+        float4 v = ld_cluster4(smem + (uint32_t)(r * (BN + 4) + c) * 4, 0);
+        for (uint32_t q = 1; q < split; ++q) {  // in rank order
+          const float4 w = ld_cluster4(smem + (uint32_t)(r * (BN + 4) + c) * 4, q);
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
+        }
+        uint16_t* dst = a.out + (o.row + r) * a.n + o.col + c;
+        const uint32_t lo = pack_bf16(__float_as_uint(v.x), __float_as_uint(v.y));
+        const uint32_t hi = pack_bf16(__float_as_uint(v.z), __float_as_uint(v.w));
+        if (vec) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+        } else {
+          dst[0] = (uint16_t)lo;
+          if (o.col + c + 1 < a.n) dst[1] = (uint16_t)(lo >> 16);
+          if (o.col + c + 2 < a.n) dst[2] = (uint16_t)hi;
+          if (o.col + c + 3 < a.n) dst[3] = (uint16_t)(hi >> 16);
+        }
+      }
+    }
+    cluster_sync();  // a peer may still be reading this CTA's sums
   }
   __syncthreads();
   if (warp == 1) {
@@ -394,19 +585,71 @@ bool code_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int box_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int STAGES>
-fp8q_status launch_matmul(const DeviceInfo& dev, const uint8_t* aq, const uint8_t* bq, const MatmulArgs& a,
+template <int BN, int STAGES, int ACC, bool SPLIT>
+fp8q_status launch_matmul(const DeviceInfo& dev, const uint8_t* aq, const uint8_t* bq, const MatmulArgs& a, int split,
                           cudaStream_t stream) {
-  using C = Cfg<BN, STAGES>;
+  using C = Cfg<BN, STAGES, ACC>;
+  static_assert(!SPLIT || kBM * (BN + 4) * 4 <= STAGES * C::kStageBytes, "the sums fit the stages");
   CUtensorMap ma, mb;
-  if (!code_map(&ma, aq, a.m, a.k, kBM) || !code_map(&mb, bq, a.n * a.groups, a.k, BN)) return FP8Q_ERR_CUDA;
-  auto kernel = mxfp4_matmul_kernel<BN, STAGES>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-    return FP8Q_ERR_CUDA;
+  if (!code_map(&ma, aq, a.m, a.k, a.a_rows) || !code_map(&mb, bq, a.n * a.groups, a.k, BN)) return FP8Q_ERR_CUDA;
+  auto kernel = mxfp4_matmul_kernel<BN, STAGES, ACC, SPLIT>;
+  static std::atomic<uint64_t> prepared{0};  // devices (below 64) whose shared-memory limit was raised
+  if (!(prepared.load(std::memory_order_relaxed) >> dev.device & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    prepared.fetch_or(1ull << dev.device, std::memory_order_relaxed);
+  }
   const int64_t tiles = (a.m + kBM - 1) / kBM * ((a.n + BN - 1) / BN);
-  const unsigned grid = (unsigned)(tiles < dev.num_sms ? tiles : dev.num_sms);
-  return launch_after(kernel, dim3(grid), kThreads, (size_t)C::kSmem, stream, ma, mb, a) == cudaSuccess ? FP8Q_OK
-                                                                                                  : FP8Q_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : tiles < dev.num_sms ? tiles : dev.num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+}
+
+// Which tile width, and how many CTAs share a tile's k.  Modelled time in ns; each CTA runs
+// `steps` stages for each of its tiles.  Measured, an SM at a time and then all of them:
+//   a stage takes 290 / 300 / 345 / 500 ns at 32 / 64 / 128 / 256 columns (the wait, four MMAs
+//   of at least 50 ns, and with every SM busy the shared-memory traffic), so the widest tile
+//   is the fastest per output (4.5 PFLOP/s at 8192x4096x7168; 3.4 at 128 columns, 1.9 at 64)
+//   as long as its tiles fill the SMs;
+//   a tile's epilogue that no other tile's MMAs cover takes about 4 ns a column;
+//   sharing k saves stages and costs the exchange of the sums: 1.2 us and 0.12 ns for each of
+//   the tile's stored elements (1x4096x7168: 11.3 us unshared at 64 columns, 7.0 us with 4
+//   CTAs at 128; 256x4096x4096: 8.2 us unshared at 64, 9.1 us with 2 at 128).  It is taken
+//   within one wave only, where the clusters are resident together.
+struct Variant {
+  int bn, split;
+};
+Variant choose(int64_t m, int64_t n, int64_t k, int sms) {
+  constexpr int kBn[4] = {256, 128, 64, 32};
+  constexpr double kStage[4] = {500, 345, 300, 290};
+  const int64_t steps = (k + kBK - 1) / kBK;
+  Variant best = {256, 1};
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t tiles = (m + kBM - 1) / kBM * ((n + kBn[i] - 1) / kBn[i]);
+    for (int s = 1; s <= 4; s *= 2) {
+      if (s > 1 && (tiles * s > sms || s > steps || kBn[i] == 32)) break;
+      const double waves = (double)((tiles * s + sms - 1) / sms);
+      double t = waves * (double)((steps + s - 1) / s) * kStage[i] + 4.0 * kBn[i] * (i == 0 ? waves : 1.0);
+      if (s > 1) t += 1200 + 0.12 * (double)(m < kBM ? m : kBM) * kBn[i];
+      if (t < least) {
+        least = t;
+        best = {kBn[i], s};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -428,6 +671,17 @@ extern "C" fp8q_status fp8q_matmul_mxfp4(const uint8_t* aq, const uint8_t* asf, 
     return FP8Q_ERR_ALIGN;
   DeviceInfo dev;
   if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
-  const MatmulArgs a = {asf, bsf, group_offsets, static_cast<uint16_t*>(out), m, n, (int)k, num_groups, dev.status};
-  return launch_matmul<128, 6>(dev, aq, bq, a, to_stream(stream));
+  const int a_rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  const MatmulArgs a = {asf, bsf, group_offsets, static_cast<uint16_t*>(out), m, n, (int)k, num_groups, a_rows, dev.status};
+  cudaStream_t st = to_stream(stream);
+  const Variant v = choose(m, n, k, dev.num_sms);
+  switch (v.bn * (v.split > 1 ? -1 : 1)) {
+    case 32: return launch_matmul<32, 9, 2, false>(dev, aq, bq, a, 1, st);
+    case 64: return launch_matmul<64, 8, 2, false>(dev, aq, bq, a, 1, st);
+    case 128: return launch_matmul<128, 6, 2, false>(dev, aq, bq, a, 1, st);
+    case 256: return launch_matmul<256, 4, 1, false>(dev, aq, bq, a, 1, st);
+    case -64: return launch_matmul<64, 8, 2, true>(dev, aq, bq, a, v.split, st);
+    case -128: return launch_matmul<128, 6, 2, true>(dev, aq, bq, a, v.split, st);
+    default: return launch_matmul<256, 4, 1, true>(dev, aq, bq, a, v.split, st);
+  }
 }
