@@ -28,6 +28,7 @@
 
 
 #include "abi_checks.h"
+#include "cluster.cuh"
 #include "launch.h"
 #include "mxfp4.cuh"
 
@@ -133,30 +134,6 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
   return r;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
 }
 
 // Shared-memory matrix descriptor (K-major, version 1): codes under the 128-byte swizzle,
@@ -600,20 +577,10 @@ fp8q_status launch_matmul(const DeviceInfo& dev, const uint8_t* aq, const uint8_
     prepared.fetch_or(1ull << dev.device, std::memory_order_relaxed);
   }
   const int64_t tiles = (a.m + kBM - 1) / kBM * ((a.n + BN - 1) / BN);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : tiles < dev.num_sms ? tiles : dev.num_sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = SPLIT ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  const unsigned grid = (unsigned)(SPLIT ? tiles * split : tiles < dev.num_sms ? tiles : dev.num_sms);
+  return launch_clusters_after(kernel, grid, (unsigned)split, kThreads, (size_t)C::kSmem, stream, ma, mb, a) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
 }
 
 // Which tile width, and how many CTAs share a tile's k.  Modelled time in ns; each CTA runs

@@ -19,13 +19,19 @@
 //   softmax: d p_e += g_e;  d l_e = p_e * (d p_e - sum_j d p_j p_j)
 //   sigmoid: d p_e += (g_e - sum_j g_j h_j) / (sum of all p + 1e-20);  d l_e = d p_e * p_e * (1 - p_e)
 //
-// One warp per token, the token's logits in registers (expert e = lane + 32 i).  Each pick
-// is a warp maximum of the order-preserving integer image of the key.  All sums are fp32
-// in a fixed order (per lane over the warp's tokens, over the CTA's warps, then over CTAs
-// in double), the counts are integers: nothing depends on the order of atomics.
+// One warp per token, the token's logits in registers (four neighbouring experts a lane and
+// 16-byte loads from 65 experts on), the next token's on their way.  The picks of a row of
+// 65 or more experts come from a short list: the k-th largest of the 32 lanes' maxima bounds
+// the k-th largest value from below, and what reaches it (a dozen, typically) is gathered
+// one to a lane, so that a pick is one warp maximum and a vote instead of a pass over the
+// row.  With a bias the list is made from fp32 scores with a margin for their rounding, and
+// only its members are scored in double.  All sums are fp32 in a fixed order (per lane over
+// the warp's tokens, over the CTA's warps, then over CTAs in double), the counts are
+// integers: nothing depends on the order of atomics.
 #include <cfloat>
 
 #include "abi_checks.h"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 
@@ -34,7 +40,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxBlocks = 592;  // a fixed cap, so that the order of the sums is the same on every device
+// CTAs that 148 SMs hold at once: four an SM (64 registers a thread) up to 256 experts, two
+// above.  A fixed number, so that the order of the sums is the same wherever it runs.
+constexpr int resident(int vpl) { return vpl <= 8 ? 4 : 2; }
+constexpr int max_blocks(int experts) { return 148 * (experts <= 256 ? resident(8) : resident(16)); }
 constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopk = 64;
 constexpr float kEps = 1e-20f;
@@ -42,24 +51,34 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 enum Mode { kSoftmax = 0, kSigmoid = 1, kSigmoidBias = 2 };
 
-__device__ __forceinline__ float load_logit(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load_logit(const uint16_t* p, int64_t i) {
-  return __uint_as_float((uint32_t)p[i] << 16);
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) {
+  return v;
 }
-__device__ __forceinline__ void store_grad(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store_grad(uint16_t* p, int64_t i, float v) {
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
-  p[i] = r;
+template <>
+__device__ __forceinline__ float to_float<uint16_t>(uint16_t v) {
+  return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// NaN counts as -inf (a padding row may hold anything), +inf as the largest finite value;
-// adding +0 turns -0 into +0, so that the two tie.
-__device__ __forceinline__ float clean(float l) { return l != l ? -INFINITY : fminf(l + 0.0f, FLT_MAX); }
+// Expert i of a lane: four neighbours a lane from four experts a lane on.
+template <int VPL>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return VPL < 4 ? lane + 32 * i : 4 * lane + 128 * (i >> 2) + (i & 3);
+}
 
-// fp32 -> uint32 with the same order; every value but NaN maps above 0.
+// NaN counts as -inf (a padding row may hold anything), +inf as the largest finite value.
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
+
+// fp32 -> uint32 with the same order (-0 and +0 equal); every value but NaN maps above 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(v + 0.0f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_key(uint32_t k) {
@@ -72,13 +91,83 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// exp(x), x <= 0, by the hardware base-2 exponential: off by 1.5 |x| + 4 half steps.
+__device__ __forceinline__ float exp_neg(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // p = sigmoid(l) and q = 1 - p without cancellation on either side.
 __device__ __forceinline__ void sigmoid2(float l, float& p, float& q) {
-  const float t = expf(-fabsf(l));
-  const float r = __frcp_rn(1.0f + t);
+  const float t = exp_neg(-fabsf(l));
+  const float r = rcp(1.0f + t);
   const float s = t * r;
   p = l >= 0.0f ? r : s;
   q = l >= 0.0f ? s : r;
+}
+
+// A token's logits as they lie in memory (padding lanes: -inf), and cleaned.
+template <int VPL, typename T>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, bool quads, float (&v)[VPL]) {
+  if (VPL >= 4 && quads) {  // E % 4 == 0: whole, aligned quads
+#pragma unroll
+    for (int j = 0; j < VPL; j += 4) {
+      const int e = expert_of<VPL>(lane, j);
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4) {
+          f = *reinterpret_cast<const float4*>(row + e);
+        } else {
+          const uint2 h = *reinterpret_cast<const uint2*>(row + e);
+          f = make_float4(__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xFFFF0000u), __uint_as_float(h.y << 16),
+                          __uint_as_float(h.y & 0xFFFF0000u));
+        }
+      }
+      v[j] = f.x;
+      if constexpr (VPL >= 4) {
+        v[j + 1] = f.y;
+        v[j + 2] = f.z;
+        v[j + 3] = f.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of<VPL>(lane, i);
+      v[i] = e < E ? to_float<T>(row[e]) : -INFINITY;
+    }
+  }
+}
+template <int VPL, typename T>
+__device__ __forceinline__ void store_row(T* __restrict__ row, int E, int lane, bool quads, const float (&v)[VPL]) {
+  if (VPL >= 4 && quads) {
+#pragma unroll
+    for (int j = 0; j < VPL; j += 4) {
+      const int e = expert_of<VPL>(lane, j);
+      if constexpr (VPL >= 4) {
+        if (e < E) {
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(row + e) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          else
+            *reinterpret_cast<uint2*>(row + e) = make_uint2(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]));
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of<VPL>(lane, i);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4) row[e] = v[i];
+        else row[e] = (T)pack_bf16(v[i], 0.0f);
+      }
+    }
+  }
 }
 
 struct RouterArgs {
@@ -88,20 +177,158 @@ struct RouterArgs {
   float scale;
 };
 
+// ------------------------------------------------------------------ selection
+struct Pick {
+  float l;  // its logit
+  int e;
+};
+
+// The score that orders experts under a bias, in double (neighbouring scores can be closer
+// than an fp32 sum resolves), as the fp32 value and the remainder.  NaN counts as -inf.
+__device__ __forceinline__ void bias_keys(float l, float bias, uint32_t& hi, uint32_t& lo) {
+  const double s = 1.0 / (1.0 + exp(-(double)l)) + (double)bias;
+  const float h = (float)s;
+  const float r = (float)(s - (double)h);
+  hi = order_key(h == h ? h : -INFINITY);
+  lo = order_key(r == r ? r : 0.0f);
+}
+
+// Any row: each pick passes over the whole row.  Writes the k picks, best first.
+template <int VPL, int MODE, typename T>
+__device__ __forceinline__ void pick_all(const T* __restrict__ row, const float* __restrict__ bias, int E, int K,
+                                         int lane, Pick* __restrict__ picks) {
+  uint32_t key[VPL];
+  uint32_t key_lo[MODE == kSigmoidBias ? VPL : 1];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = expert_of<VPL>(lane, i);
+    key[i] = 0u;
+    if (MODE == kSigmoidBias) key_lo[i] = 0u;
+    if (e < E) {
+      const float l = clean(to_float<T>(row[e]));
+      if (MODE == kSigmoidBias) bias_keys(l, bias[e], key[i], key_lo[i]);
+      else key[i] = order_key(l);
+    }
+  }
+  for (int s = 0; s < K; ++s) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
+    const uint32_t m = __reduce_max_sync(kAll, best);
+    uint32_t m_lo = 0u;
+    if (MODE == kSigmoidBias) {
+      uint32_t b = 0u;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] == m) b = max(b, key_lo[i]);
+      m_lo = __reduce_max_sync(kAll, b);
+    }
+    uint32_t e = 0xFFFFu;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = expert_of<VPL>(lane, i);
+    e = __reduce_min_sync(kAll, e);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e == (uint32_t)expert_of<VPL>(lane, i)) key[i] = 0u;
+    if (lane == 0) {
+      picks[s].e = (int)e;
+      picks[s].l = MODE == kSigmoidBias ? clean(to_float<T>(row[e])) : from_key(m);
+    }
+  }
+  __syncwarp();
+}
+template <int VPL, int MODE, typename T>
+__device__ __noinline__ void pick_all_call(const T* row, const float* bias, int E, int K, int lane, Pick* picks) {
+  pick_all<VPL, MODE, T>(row, bias, E, K, lane, picks);
+}
+
+// How far an fp32 score sigmoid2(l) + bias may be from the exact one: the sigmoid by 2^-21
+// (1.5 |l| + 4 half steps of the exponential times s (1 - s), and 4 more, are 5.4 half steps),
+// the sum by half a step; the rest covers the arithmetic on the bound itself.
+__device__ __forceinline__ float score_error(float score) { return 0x1.4p-21f + 0x1p-23f * fabsf(score); }
+
+constexpr int kListTopk = 16;  // the short list is tried up to this k (it needs k <= 32 lanes)
+
+// From the short list: `order` holds what the row is ordered by (the logits, or fp32 scores
+// under a bias), `val` the logits.  false (nothing written) if the list would not fit.
+template <int VPL, int MODE>
+__device__ __forceinline__ bool pick_listed(const float (&order)[VPL], const float (&val)[VPL],
+                                            const float* __restrict__ bias, int K, int lane, Pick* __restrict__ picks) {
+  float lm = order[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) lm = fmaxf(lm, order[i]);
+  uint32_t cur = order_key(lm), m = 0u;
+  for (int s = 0; s < K; ++s) {
+    m = __reduce_max_sync(kAll, cur);
+    if (lane == __ffs(__ballot_sync(kAll, cur == m)) - 1) cur = 0u;
+  }
+  float least = from_key(m);
+  if (MODE == kSigmoidBias) least -= 2.0f * score_error(least);  // loosened by the errors on either side
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool in = order[i] >= least;
+    const unsigned mask = __ballot_sync(kAll, in);
+    const int at = n + __popc(mask & ((1u << lane) - 1u));
+    if (in && at < 32) {
+      picks[at].l = val[i];
+      picks[at].e = expert_of<VPL>(lane, i);
+    }
+    n += __popc(mask);
+  }
+  __syncwarp();
+  if (n > 32 || !(least > -INFINITY)) {  // (a bound of -inf, or NaN, lets padding lanes in)
+    __syncwarp();
+    return false;
+  }
+  Pick c = {0.0f, 0xFFFF};
+  if (lane < n) c = picks[lane];
+  __syncwarp();
+  uint32_t key = 0u, lo = 0u;
+  if (lane < n) {
+    if (MODE == kSigmoidBias) bias_keys(c.l, bias[c.e], key, lo);
+    else key = order_key(c.l);
+  }
+  for (int s = 0; s < K; ++s) {
+    const uint32_t top = __reduce_max_sync(kAll, key);
+    bool won = key == top;
+    const unsigned b = __ballot_sync(kAll, won);
+    if (b & (b - 1u)) {  // equal keys: the remainder, then the lowest id
+      if (MODE == kSigmoidBias) {
+        const uint32_t t2 = __reduce_max_sync(kAll, won ? lo : 0u);
+        won = won && lo == t2;
+      }
+      const uint32_t e = __reduce_min_sync(kAll, won ? (uint32_t)c.e : 0xFFFFFFFFu);
+      won = won && (uint32_t)c.e == e;
+    }
+    if (won) {
+      picks[s] = c;
+      key = 0u;
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
 // ------------------------------------------------------------------ forward
 // Workspace: [0] a counter for the finishing kernel, then per CTA E sums (fp32), then per
 // CTA E counts (int32), from byte 16 on.
 template <int VPL, int MODE, typename T>
-__global__ void __launch_bounds__(kThreads) router_kernel(const T* __restrict__ logits, const float* __restrict__ bias,
+__global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T* __restrict__ logits, const float* __restrict__ bias,
                                                           const uint8_t* __restrict__ mask, RouterArgs a,
                                                           int32_t* __restrict__ topk_idx, float* __restrict__ weights,
                                                           uint32_t* __restrict__ ws) {
-  __shared__ float sums_sh[kRouterMaxExperts];
-  __shared__ int counts_sh[kRouterMaxExperts];
+  constexpr int kSlots = 32 * VPL;
+  __shared__ float sums_sh[kSlots];
+  __shared__ int counts_sh[kSlots];
+  __shared__ Pick picks_sh[kWarps][kRouterMaxTopk];
   pdl_wait_for(logits, bias, mask);
   pdl_trigger();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int E = a.E, K = a.topk;
+  const bool quads = (E & 3) == 0, bias_quads = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
+  Pick* picks = picks_sh[wid];
   float acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
@@ -112,68 +339,53 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const T* __restrict__ 
     }
     __syncthreads();
   }
+  constexpr bool kAhead = VPL <= 8;  // the next row is loaded while this one is worked on
   const int64_t stride = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + wid; t < a.tokens; t += stride) {
+  int64_t t = (int64_t)blockIdx.x * kWarps + wid;
+  float next[VPL];
+  if (kAhead && t < a.tokens) load_row<VPL, T>(logits + t * E, E, lane, quads, next);
+  for (; t < a.tokens; t += stride) {
+    const T* row = logits + t * E;
     const bool live = mask == nullptr || mask[t] != 0;
-    uint32_t key[VPL];
-    uint32_t key_lo[MODE == kSigmoidBias ? VPL : 1];
-    float val[VPL];  // the logit, then its share of the balance statistics
+    float val[VPL];
+    if (kAhead) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      val[i] = -INFINITY;
-      key[i] = 0u;
-      if (MODE == kSigmoidBias) key_lo[i] = 0u;
-      if (e < E) {
-        val[i] = clean(load_logit(logits, t * E + e));
+      for (int i = 0; i < VPL; ++i) val[i] = clean(next[i]);
+      if (t + stride < a.tokens) load_row<VPL, T>(row + stride * E, E, lane, quads, next);
+    } else {
+      load_row<VPL, T>(row, E, lane, quads, val);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) val[i] = clean(val[i]);
+    }
+    float p[VPL];
+    if (MODE != kSoftmax && (MODE == kSigmoidBias || a.stats)) {
+      float q;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sigmoid2(val[i], p[i], q);
+    }
+    // ---- the k picks
+    if constexpr (VPL < 4) {
+      pick_all<VPL, MODE, T>(row, bias, E, K, lane, picks);
+    } else {
+      bool done = false;
+      if (K <= kListTopk) {
         if (MODE == kSigmoidBias) {
-          // Neighbouring scores can be closer than an fp32 sum resolves: the score is
-          // formed in double and compared as its fp32 value and the remainder.
-          const double s = 1.0 / (1.0 + exp(-(double)val[i])) + (double)bias[e];
-          const float hi = (float)s;
-          key[i] = max(order_key(hi + 0.0f), 1u);
-          key_lo[i] = order_key((float)(s - (double)hi) + 0.0f);
+          float order[VPL];
+          load_row<VPL, float>(bias, E, lane, quads && bias_quads, order);  // (padding lanes: -inf)
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) order[i] += p[i];
+          done = pick_listed<VPL, MODE>(order, val, bias, K, lane, picks);
         } else {
-          key[i] = order_key(val[i]);
+          done = pick_listed<VPL, MODE>(val, val, bias, K, lane, picks);
         }
       }
+      if (!done) pick_all_call<VPL, MODE, T>(row, bias, E, K, lane, picks);
     }
-    // ---- the k picks: lane s (and 32 + s) keeps pick s
-    int pick_e[2] = {0, 0};
-    float pick_v[2] = {-INFINITY, -INFINITY};
-    float top = -INFINITY;
-    for (int s = 0; s < K; ++s) {
-      uint32_t best = key[0];
+    Pick mine[2];
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
-      const uint32_t m = __reduce_max_sync(kAll, best);
-      uint32_t m_lo = 0u;
-      if (MODE == kSigmoidBias) {
-        uint32_t b = 0u;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[i] == m) b = max(b, key_lo[i]);
-        m_lo = __reduce_max_sync(kAll, b);
-      }
-      uint32_t e = 0xFFFFu;
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = lane + 32 * i;
-      e = __reduce_min_sync(kAll, e);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (e == (uint32_t)(lane + 32 * i)) key[i] = 0u;
-      if (s == 0 && MODE == kSoftmax) top = from_key(m);
-      if (lane == (s & 31)) {
-        if (s < 32) {
-          pick_e[0] = (int)e;
-          pick_v[0] = from_key(m);
-        } else {
-          pick_e[1] = (int)e;
-          pick_v[1] = from_key(m);
-        }
-      }
-    }
+    for (int h = 0; h < 2; ++h) mine[h] = lane + 32 * h < K ? picks[lane + 32 * h] : Pick{-INFINITY, 0};
+    const float top = picks[0].l;
+    __syncwarp();
     // ---- probabilities
     float z_inv = 1.0f;  // softmax: 1 / sum exp
     if (MODE == kSoftmax) {
@@ -182,57 +394,49 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const T* __restrict__ 
         const float base = top == -INFINITY ? 0.0f : top;  // a row of -inf has no probability at all
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          val[i] = expf(val[i] - base);
-          z += val[i];
+          p[i] = exp_neg(val[i] - base);
+          z += p[i];
         }
         z = warp_sum(z);
-        z_inv = z > 0.0f ? __frcp_rn(z) : 0.0f;
+        z_inv = z > 0.0f ? rcp(z) : 0.0f;
+        if (a.stats && live) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) val[i] *= z_inv;
+          for (int i = 0; i < VPL; ++i) acc[i] = __fmaf_rn(p[i], z_inv, acc[i]);
+        }
       }
     } else if (a.stats) {
-      float z = 0.0f, q;
+      float z = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        sigmoid2(val[i], val[i], q);
-        z += val[i];
-      }
-      z = warp_sum(z) + kEps;
-      z_inv = __frcp_rn(z);
+      for (int i = 0; i < VPL; ++i) z += p[i];
+      const float share = live ? rcp(warp_sum(z) + kEps) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) val[i] *= z_inv;
-    }
-    if (a.stats && live) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] += val[i];
+      for (int i = 0; i < VPL; ++i) acc[i] = __fmaf_rn(p[i], share, acc[i]);
     }
     float w[2], total = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool on = lane + 32 * h < K;
       w[h] = 0.0f;
-      if (on) {
+      if (lane + 32 * h < K) {
         if (MODE == kSoftmax) {
-          w[h] = top == -INFINITY ? 0.0f : expf(pick_v[h] - top);
+          w[h] = top == -INFINITY ? 0.0f : exp_neg(mine[h].l - top);
           if (!a.renorm) w[h] *= z_inv;
         } else {
           float q;
-          const float l = MODE == kSigmoidBias ? clean(load_logit(logits, t * E + pick_e[h])) : pick_v[h];
-          sigmoid2(l, w[h], q);
+          sigmoid2(mine[h].l, w[h], q);
         }
       }
       total += w[h];
     }
     // The eps is of the size of the probabilities; exp(l - max) exceeds them by the factor
     // z >= 1, for which 1e-20 is as far below fp32 resolution.
-    const float factor = a.renorm ? a.scale * __frcp_rn(warp_sum(total) + kEps) : a.scale;
+    const float factor = a.renorm ? a.scale * rcp(warp_sum(total) + kEps) : a.scale;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int s = lane + 32 * h;
       if (s < K) {
-        topk_idx[t * K + s] = pick_e[h];
+        topk_idx[t * K + s] = mine[h].e;
         weights[t * K + s] = live ? w[h] * factor : 0.0f;
-        if (a.stats && live) atomicAdd(&counts_sh[pick_e[h]], 1);
+        if (a.stats && live) atomicAdd(&counts_sh[mine[h].e], 1);
       }
     }
   }
@@ -241,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const T* __restrict__ 
     if (wid == w) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) sums_sh[lane + 32 * i] += acc[i];
+        if (expert_of<VPL>(lane, i) < E) sums_sh[expert_of<VPL>(lane, i)] += acc[i];
     }
     __syncthreads();
   }
@@ -254,25 +458,29 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const T* __restrict__ 
   if (blockIdx.x == 0 && threadIdx.x == 0) ws[0] = 0u;
 }
 
-// Sums the CTAs' partial results: a CTA per 32 experts, a warp per every 32nd CTA's row;
-// the last CTA to finish (the counter was zeroed by the kernel before) forms the loss.
-__global__ void __launch_bounds__(1024) router_finish_kernel(int blocks, int E, int topk, float loss_coef,
-                                                             uint32_t* __restrict__ ws, int32_t* __restrict__ counts,
-                                                             float* __restrict__ prob_sums, float* __restrict__ loss) {
-  __shared__ double sum_sh[32][33];
-  __shared__ int cnt_sh[32][33];
+// Sums the CTAs' partial results: a cluster of CTAs per 32 experts, its warps sharing the
+// rows (10 each at most, all on their way at once), the CTAs' sums joined in rank order; the
+// last cluster to finish (the counter was zeroed by the kernel before) forms the loss.
+constexpr int kFinishCluster = 8;
+__global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int E, int topk, float loss_coef,
+                                                                 uint32_t* __restrict__ ws, int32_t* __restrict__ counts,
+                                                                 float* __restrict__ prob_sums,
+                                                                 float* __restrict__ loss) {
+  __shared__ double sum_sh[kWarps][32];
+  __shared__ int cnt_sh[kWarps][32];
   __shared__ bool last;
   pdl_wait_for(ws, counts, prob_sums);
   pdl_trigger();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + lane;
+  const uint32_t size = cluster_size(), rank = cluster_rank();
+  const int e = blockIdx.x / size * 32 + lane;
   const float* part = reinterpret_cast<const float*>(ws + 4);
   const int32_t* part_n = reinterpret_cast<const int32_t*>(part + (int64_t)blocks * E);
   double s = 0.0;
   int n = 0;
   if (e < E) {
-#pragma unroll 4
-    for (int b = wid; b < blocks; b += 32) {
+#pragma unroll 10
+    for (int b = rank * kWarps + wid; b < blocks; b += size * kWarps) {
       s += (double)part[(int64_t)b * E + e];
       n += part_n[(int64_t)b * E + e];
     }
@@ -280,19 +488,36 @@ __global__ void __launch_bounds__(1024) router_finish_kernel(int blocks, int E, 
   sum_sh[wid][lane] = s;
   cnt_sh[wid][lane] = n;
   __syncthreads();
-  if (wid == 0 && e < E) {
-    for (int w = 1; w < 32; ++w) {
+  if (wid == 0) {
+    for (int w = 1; w < kWarps; ++w) {
       s += sum_sh[w][lane];
       n += cnt_sh[w][lane];
     }
+    sum_sh[0][lane] = s;
+    cnt_sh[0][lane] = n;
+  }
+  if (size > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0 && wid == 0) {
+      for (uint32_t r = 1; r < size; ++r) {
+        s += ld_cluster_f64(smem_u32(&sum_sh[0][lane]), r);
+        n += ld_cluster_s32(smem_u32(&cnt_sh[0][lane]), r);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the peers' sums were read: they may end
+  }
+  if (rank != 0 || wid != 0) return;
+  if (e < E) {
     counts[e] = n;
     prob_sums[e] = (float)s;
     __threadfence();
   }
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(ws, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last || wid != 0) return;
+  __syncwarp();
+  if (lane == 0) last = atomicAdd(ws, 1u) == gridDim.x / size - 1;
+  __syncwarp();
+  if (!last) return;
   __threadfence();
   double dot = 0.0;
   long long c = 0;
@@ -311,7 +536,7 @@ __global__ void __launch_bounds__(1024) router_finish_kernel(int blocks, int E, 
 
 // ------------------------------------------------------------------ backward
 template <int VPL, bool SIGMOID, typename T>
-__global__ void __launch_bounds__(kThreads) router_bwd_kernel(const T* __restrict__ logits,
+__global__ void __launch_bounds__(kThreads, resident(VPL)) router_bwd_kernel(const T* __restrict__ logits,
                                                               const uint8_t* __restrict__ mask, RouterArgs a,
                                                               const int32_t* __restrict__ topk_idx,
                                                               const float* __restrict__ grad_weights,
@@ -319,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const T* __restric
                                                               const int32_t* __restrict__ counts, float loss_coef,
                                                               const float* __restrict__ grad_loss,
                                                               T* __restrict__ grad, int* status) {
-  extern __shared__ float sh[];  // [E] g_e, then per warp [E]
+  extern __shared__ __align__(16) float sh[];  // g_e, then a row per warp
   __shared__ long long c_sh[kWarps];
   pdl_wait_for(logits, mask, topk_idx, grad_weights, row_id_map, counts, grad_loss);
   pdl_trigger();
@@ -327,7 +552,8 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const T* __restric
   const int E = a.E, K = a.topk;
   const bool balance = grad_loss != nullptr;
   float* g_sh = sh;
-  float* buf = sh + E + wid * E;
+  const int pitch = (E + 3) & ~3;  // rows on 16 bytes
+  float* buf = sh + (1 + wid) * pitch;
   if (balance) {
     long long c = 0;
     for (int e = threadIdx.x; e < E; e += kThreads) c += counts[e];
@@ -341,151 +567,188 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const T* __restric
     for (int e = threadIdx.x; e < E; e += kThreads) g_sh[e] = (float)(f * (double)counts[e]);
     __syncthreads();
   }
+  float g[VPL];  // this lane's g_e
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) g[i] = balance && expert_of<VPL>(lane, i) < E ? g_sh[expert_of<VPL>(lane, i)] : 0.0f;
+  const bool quads = (E & 3) == 0;
+  // A row of zeros per warp, into which the chosen experts' gradients are put and taken out
+  // again.
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (expert_of<VPL>(lane, i) < E) buf[expert_of<VPL>(lane, i)] = 0.0f;
+  __syncwarp();
+  constexpr bool kAhead = VPL <= 8;
   const int64_t stride = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + wid; t < a.tokens; t += stride) {
+  int64_t t = (int64_t)blockIdx.x * kWarps + wid;
+  float next[VPL];
+  if (kAhead && t < a.tokens) load_row<VPL, T>(logits + t * E, E, lane, quads, next);
+  int next_id[2] = {-1, -1};  // this lane's slots of the next token: expert (or -1), gradient
+  float next_dw[2] = {0.0f, 0.0f};
+  auto load_slots = [&](int64_t u) {
+    if (grad_weights == nullptr || (mask != nullptr && mask[u] == 0)) return;  // (a masked token's are not used)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int s = lane + 32 * h;
+      if (s < K) {
+        const int e = topk_idx[u * K + s];
+        int64_t at = u * K + s;
+        bool ok = e >= 0 && e < E;
+        if (row_id_map != nullptr) {
+          at = row_id_map[at];
+          ok = ok && at >= 0 && at < rows;
+        }
+        next_id[h] = ok ? e : -1;
+        next_dw[h] = ok ? grad_weights[at] : 0.0f;
+        if (!ok) record_status(status, FP8Q_ERR_DEVICE);
+      }
+    }
+  };
+  if (t < a.tokens) load_slots(t);
+  for (; t < a.tokens; t += stride) {
+    const T* row = logits + t * E;
+    float p[VPL];
+    if (kAhead) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] = clean(next[i]);
+      if (t + stride < a.tokens) load_row<VPL, T>(row + stride * E, E, lane, quads, next);
+    } else {
+      load_row<VPL, T>(row, E, lane, quads, p);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] = clean(p[i]);
+    }
     if (mask != nullptr && mask[t] == 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) store_grad(grad, t * E + lane + 32 * i, 0.0f);
+      for (int i = 0; i < VPL; ++i) p[i] = 0.0f;
+      store_row<VPL, T>(grad + t * E, E, lane, quads, p);
+      if (t + stride < a.tokens) load_slots(t + stride);
       continue;
     }
-    float p[VPL], q[SIGMOID ? VPL : 1];
-    float z = 0.0f;
+    // ---- the slots: lane s (and 32 + s) holds slot s
+    int id[2];
+    float dw[2], ps[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      id[h] = next_id[h];
+      dw[h] = next_dw[h];
+      ps[h] = id[h] >= 0 ? clean(to_float<T>(row[id[h]])) : 0.0f;
+    }
+    if (t + stride < a.tokens) load_slots(t + stride);
+    // ---- probabilities (softmax: not yet divided by their sum) and the row's sums
+    float q[SIGMOID ? VPL : 1], unused;
     if (SIGMOID) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        sigmoid2(e < E ? clean(load_logit(logits, t * E + e)) : -INFINITY, p[i], q[i]);
-        z += p[i];
-      }
-      z = warp_sum(z) + kEps;
-    } else {
-      float m = -INFINITY;
+      for (int i = 0; i < VPL; ++i) sigmoid2(p[i], p[i], q[i]);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        p[i] = e < E ? clean(load_logit(logits, t * E + e)) : -INFINITY;
-        m = fmaxf(m, p[i]);
+      for (int h = 0; h < 2; ++h) {
+        if (id[h] >= 0) sigmoid2(ps[h], ps[h], unused);
       }
+    } else {
+      float m = p[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, p[i]);
       m = from_key(__reduce_max_sync(kAll, order_key(m)));
       const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        p[i] = expf(p[i] - base);
-        z += p[i];
-      }
-      z = warp_sum(z);
-      const float z_inv = z > 0.0f ? __frcp_rn(z) : 0.0f;
+      for (int i = 0; i < VPL; ++i) p[i] = exp_neg(p[i] - base);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) p[i] *= z_inv;
+      for (int h = 0; h < 2; ++h)
+        if (id[h] >= 0) ps[h] = exp_neg(ps[h] - base);
+    }
+    float z = 0.0f, gp = 0.0f, total = ps[0] + ps[1], dot = dw[0] * ps[0] + dw[1] * ps[1];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) z += p[i];
+    if (balance) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) gp = __fmaf_rn(g[i], p[i], gp);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {  // four independent sums a step
+      z = __fadd_rn(z, __shfl_xor_sync(kAll, z, o));
+      gp = __fadd_rn(gp, __shfl_xor_sync(kAll, gp, o));
+      total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+      dot = __fadd_rn(dot, __shfl_xor_sync(kAll, dot, o));
+    }
+    const float z_inv = SIGMOID ? rcp(z + kEps) : (z > 0.0f ? rcp(z) : 0.0f);
+    // Softmax probabilities carry the factor z_inv: in P = sum of the chosen p + 1e-20, and
+    // in mean = sum dw p / P.
+    const float unit = SIGMOID ? 1.0f : z_inv;
+    const float inv = a.renorm ? rcp(total * unit + kEps) : 1.0f;
+    const float mean = a.renorm ? dot * unit * inv : 0.0f;
+    const float own = a.scale * inv;
+    // ---- the chosen experts' part, through the warp's row
+    if (grad_weights != nullptr) {
+      // Ids are distinct in a row the router wrote; should a caller repeat one, the slots are
+      // added one by one, in slot order.
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (id[h] >= 0) buf[id[h]] = __int_as_float(1 + lane + 32 * h);
+      __syncwarp();
+      bool repeated = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        repeated |= id[h] >= 0 && __float_as_int(buf[id[h]]) != 1 + lane + 32 * h;
+      __syncwarp();
+      if (!__any_sync(kAll, repeated)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (id[h] >= 0) buf[id[h]] = own * (dw[h] - mean);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (id[h] >= 0) buf[id[h]] = 0.0f;
+        __syncwarp();
+        for (int s = 0; s < K; ++s) {
+          const int e = s < 32 ? id[0] : id[1];
+          if (lane == (s & 31) && e >= 0) buf[e] += own * ((s < 32 ? dw[0] : dw[1]) - mean);
+          __syncwarp();
+        }
+      }
+      __syncwarp();
     }
     float d[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
     if (grad_weights != nullptr) {
+      if (VPL >= 4 && quads) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) buf[lane + 32 * i] = p[i];
-      __syncwarp();
-      int id[2];
-      float dw[2], ps[2], total = 0.0f, dot = 0.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int s = lane + 32 * h;
-        id[h] = -1;
-        dw[h] = ps[h] = 0.0f;
-        if (s < K) {
-          const int e = topk_idx[t * K + s];
-          int64_t at = t * K + s;
-          bool ok = e >= 0 && e < E;
-          if (row_id_map != nullptr) {
-            at = row_id_map[at];
-            ok = ok && at >= 0 && at < rows;
-          }
-          if (ok) {
-            id[h] = e;
-            dw[h] = grad_weights[at];
-            ps[h] = buf[e];
-          } else {
-            record_status(status, FP8Q_ERR_DEVICE);
+        for (int j = 0; j < VPL; j += 4) {
+          if constexpr (VPL >= 4) {
+            if (expert_of<VPL>(lane, j) < E) {
+              const float4 f = *reinterpret_cast<const float4*>(buf + expert_of<VPL>(lane, j));
+              d[j] = f.x;
+              d[j + 1] = f.y;
+              d[j + 2] = f.z;
+              d[j + 3] = f.w;
+            }
           }
         }
-        total += ps[h];
-        dot += dw[h] * ps[h];
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) buf[lane + 32 * i] = 0.0f;
-      __syncwarp();
-      float inv = 1.0f, mean = 0.0f;
-      if (a.renorm) {
-        inv = __frcp_rn(warp_sum(total) + kEps);
-        mean = warp_sum(dot) * inv;
-      }
-      // Ids are distinct for a row the router wrote, so the stores do not meet; should a
-      // caller repeat one, the slots are added one by one, in slot order.
-      bool repeated = false;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const unsigned same = __match_any_sync(kAll, id[h] >= 0 ? id[h] : -1 - lane);
-        repeated |= __popc(same) > 1;
-      }
-      if (K > 32) {
-        for (int o = 0; o < 32; ++o) {
-          const int other = __shfl_sync(kAll, id[0], o);
-          repeated |= id[1] >= 0 && other == id[1];
-        }
-      }
-      if (!__any_sync(kAll, repeated)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (id[h] >= 0) buf[id[h]] = a.scale * inv * (dw[h] - mean);
       } else {
-        for (int s = 0; s < K; ++s) {
-          if (lane == (s & 31)) {
-            const int h = s >> 5;
-            const int e = h ? id[1] : id[0];
-            const float v = h ? dw[1] : dw[0];
-            if (e >= 0) buf[e] += a.scale * inv * (v - mean);
-          }
-          __syncwarp();
-        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (expert_of<VPL>(lane, i) < E) d[i] = buf[expert_of<VPL>(lane, i)];
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < E) d[i] = buf[lane + 32 * i];
-      __syncwarp();
+      for (int h = 0; h < 2; ++h)
+        if (id[h] >= 0) buf[id[h]] = 0.0f;
     }
+    // ---- through the scores
     if (SIGMOID) {
       if (balance) {
-        const float z_inv = __frcp_rn(z);
-        float dot = 0.0f;
+        const float base = gp * z_inv;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane + 32 * i < E) dot = __fmaf_rn(g_sh[lane + 32 * i], p[i], dot);
-        dot = warp_sum(dot) * z_inv;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane + 32 * i < E) d[i] = __fmaf_rn(g_sh[lane + 32 * i] - dot, z_inv, d[i]);
+        for (int i = 0; i < VPL; ++i) d[i] = __fmaf_rn(g[i] - base, z_inv, d[i]);
       }
 #pragma unroll
       for (int i = 0; i < VPL; ++i) d[i] *= p[i] * q[i];
     } else {
-      float dot = 0.0f;
+      // sum d p: the balance part over all experts, and the slots' own * (dw - mean) p
+      const float all = __fmaf_rn(own * unit, dot - mean * total, gp * unit);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (balance && lane + 32 * i < E) d[i] += g_sh[lane + 32 * i];
-        dot = __fmaf_rn(d[i], p[i], dot);
-      }
-      dot = warp_sum(dot);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) d[i] = p[i] * (d[i] - dot);
+      for (int i = 0; i < VPL; ++i) d[i] = (p[i] * unit) * ((balance ? d[i] + g[i] : d[i]) - all);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 32 * i < E) store_grad(grad, t * E + lane + 32 * i, d[i]);
+    store_row<VPL, T>(grad + t * E, E, lane, quads, d);
+    __syncwarp();
   }
 }
 
@@ -513,9 +776,9 @@ __global__ void __launch_bounds__(256) scatter_weights_kernel(const float* __res
   row_weights[r] = weights[i];
 }
 
-int router_blocks(int64_t tokens) {
+int router_blocks(int64_t tokens, int experts) {
   const int64_t b = (tokens + kWarps - 1) / kWarps;
-  return (int)(b < 1 ? 1 : b < kMaxBlocks ? b : kMaxBlocks);
+  return (int)(b < 1 ? 1 : b < max_blocks(experts) ? b : max_blocks(experts));
 }
 
 template <int VPL, typename T>
@@ -553,8 +816,8 @@ template <int VPL, typename T>
 cudaError_t launch_bwd(bool sigmoid, const T* logits, const RouterArgs& a, const BwdPtrs& p, T* grad, int* status,
                        cudaStream_t st) {
   auto k = sigmoid ? router_bwd_kernel<VPL, true, T> : router_bwd_kernel<VPL, false, T>;
-  const size_t smem = (size_t)(kWarps + 1) * a.E * sizeof(float);  // at most 36 KB
-  return launch_after(k, dim3((unsigned)router_blocks(a.tokens)), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
+  const size_t smem = (size_t)(kWarps + 1) * ((a.E + 3) & ~3) * sizeof(float);  // at most 36 KB
+  return launch_after(k, dim3((unsigned)router_blocks(a.tokens, a.E)), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
                       p.map, p.rows, p.counts, p.loss_coef, p.grad_loss, grad, status);
 }
 
@@ -591,7 +854,7 @@ extern "C" {
 
 size_t fp8q_router_workspace_bytes(int64_t tokens, int32_t num_experts) {
   if (tokens < 0 || num_experts < 1 || num_experts > kRouterMaxExperts) return 0;
-  return 16 + (size_t)router_blocks(tokens) * num_experts * 8;
+  return 16 + (size_t)router_blocks(tokens, num_experts) * num_experts * 8;
 }
 
 fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_experts, uint32_t flags,
@@ -617,7 +880,7 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
   if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
   const RouterArgs a = {tokens, num_experts, topk, (flags & FP8Q_ROUTER_RENORM) != 0, stats, scale};
   const int mode = !(flags & FP8Q_ROUTER_SIGMOID) ? kSoftmax : bias ? kSigmoidBias : kSigmoid;
-  const int blocks = router_blocks(tokens);
+  const int blocks = router_blocks(tokens, num_experts);
   uint32_t* ws = stats ? static_cast<uint32_t*>(workspace) : nullptr;
   cudaStream_t st = to_stream(stream);
   const cudaError_t rc =
@@ -626,8 +889,11 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
           : launch_fwd_for<float>(mode, blocks, logits, bias, token_mask, a, topk_idx, weights, ws, st);
   if (rc != cudaSuccess) return FP8Q_ERR_CUDA;
   if (!stats) return FP8Q_OK;
-  return launch_after(router_finish_kernel, dim3((unsigned)((num_experts + 31) / 32)), 1024, 0, st, blocks,
-                      (int)num_experts, (int)topk, loss_coef, ws, counts, prob_sums, loss) == cudaSuccess
+  // Few rows need no cluster: 64 are one or two a warp.
+  const unsigned size = blocks > 64 ? kFinishCluster : blocks > kWarps ? 2 : 1;
+  return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st,
+                               blocks, (int)num_experts, (int)topk, loss_coef, ws, counts, prob_sums,
+                               loss) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }

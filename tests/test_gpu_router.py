@@ -252,3 +252,22 @@ def test_wrong_tensors_are_refused():
         sat.router_topk(l, 33)
     with pytest.raises(sat.Fp8qError):
         sat.router_topk(l, 4, bias=torch.zeros(32, device="cuda"))  # a bias needs sigmoid scores
+
+
+@pytest.mark.parametrize("E,K", [(72, 6), (256, 8), (500, 16), (1000, 3)])
+def test_scores_apart_by_less_than_fp32_errors(E, K):
+    """Clusters of scores 2^-24 to 2^-30 apart around the border of the choice, beside well
+    separated rows: fp32 scores alone would order some of them wrongly."""
+    g = torch.Generator().manual_seed(E)
+    T = 700
+    l = make(T, E, E + 1)
+    near_l = 0.3 + torch.randint(0, 64, (T, E), generator=g).float() * 2.0 ** -25
+    rows = torch.arange(T) % 3 != 0
+    pick = torch.rand((T, E), generator=g) < 20.0 / E
+    l = torch.where(rows[:, None] & pick, near_l, l.clamp_max(0.2))
+    for scale in (0.0, 2.0 ** -26, 0.1):
+        bias = torch.randn(E, generator=g) * scale
+        check(l, K, sigmoid=True, bias=bias)
+    check(l, K, sigmoid=True, bias=torch.full((E,), 3.0e4))   # sums that lose the low bits of the scores
+    check(l, K, sigmoid=True)
+    check(l, K)
