@@ -425,8 +425,8 @@ fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id
  * fp8q_swiglu_quant_stash: y = silu(gate) * up as in fp8q_swiglu_quant, times
  * row_weights[row] when given (one more fp32 rounding; a routing weight carried here makes
  * the combine an unweighted sum).
- *   q, sf, qt, sft : as fp8q_swiglu_quant (qt, sft both NULL or both given); without
- *                    row_weights byte for byte its results.
+ *   q, sf          : as fp8q_swiglu_quant, without row_weights byte for byte its results
+ *                    (fp8q_direct_transpose gives the column-wise layout).
  *   gq, gsf, uq, usf : out, the row-wise pairs of fp8q_quantize_rowwise(gate) and (up).
  *   row_weights    : fp32 [rows] or NULL (all ones); finite.
  *
@@ -446,8 +446,8 @@ fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id
  * Errors: NULL, ALIGN, SHAPE, ARG (only one of a pair, drow_weights without row_weights),
  * CUDA. */
 fp8q_status fp8q_swiglu_quant_stash(const void *gate, const void *up, const float *row_weights, int64_t rows,
-                                    int64_t cols, uint8_t *q, uint8_t *sf, uint8_t *qt, uint8_t *sft, uint8_t *gq,
-                                    uint8_t *gsf, uint8_t *uq, uint8_t *usf, fp8q_stream_t stream);
+                                    int64_t cols, uint8_t *q, uint8_t *sf, uint8_t *gq, uint8_t *gsf, uint8_t *uq,
+                                    uint8_t *usf, fp8q_stream_t stream);
 fp8q_status fp8q_swiglu_bwd(const uint8_t *gq, const uint8_t *gsf, const uint8_t *uq, const uint8_t *usf,
                             const float *row_weights, const void *dy, int64_t rows, int64_t cols, void *dgate,
                             void *dup, float *drow_weights, fp8q_stream_t stream);

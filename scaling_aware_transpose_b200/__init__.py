@@ -84,7 +84,7 @@ def lib() -> ctypes.CDLL:
                                  ctypes.c_int),
             "fp8q_router_topk_bwd": ([P, I64, I32, ctypes.c_uint32, P, I32, F32, P, P, P, I64, P, F32, P, P, P],
                                      ctypes.c_int),
-            "fp8q_swiglu_quant_stash": ([P, P, P, I64, I64, P, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "fp8q_swiglu_quant_stash": ([P, P, P, I64, I64, P, P, P, P, P, P, P], ctypes.c_int),
             "fp8q_swiglu_bwd": ([P, P, P, P, P, P, I64, I64, P, P, P, P], ctypes.c_int),
             "fp8q_swiglu_bwd_quant": ([P, P, P, P, P, P, I64, I64, P, P, P, P, P, P, P, P], ctypes.c_int),
             "fp8q_mxfp4_sf_bytes": ([I64, I64], SZ),

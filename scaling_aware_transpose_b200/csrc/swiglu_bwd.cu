@@ -9,10 +9,18 @@
 // direct transpose take, with y in the same form on request (the products' weight gradient
 // needs it, so the forward need not keep it).
 //
-// Eight lanes per 1x128 tile, 16 elements each (one 16-byte load of either code, two of dy).
-// A CTA holds whole rows: 32 / tiles rows of up to 32 tiles, or one row in steps of 32
-// tiles, so that d w is summed inside the CTA in a fixed order.  Per element 4 B are read
-// and 4 B (BF16) or 2 to 3 B (E4M3) written: the kernel is bound by HBM.
+// A warp per row (two or four rows of one or two tiles): eight lanes per 1x128 tile, 16
+// elements each, four tiles a pass, the next pass's loads in flight during this one.  d w is
+// then a sum over the warp's lanes in a fixed order, and nothing waits for another warp.
+// Per element 4 B are read and 4 B (BF16) or 2 to 3 B (E4M3) written.  The BF16 form moves
+// them at 6.2 TB/s (86.6 us at [32768, 2048]); the E4M3 form at 4.9 TB/s (96 us), bound by
+// the issue of about 40 instructions an element at 20 warps an SM (96 registers: fewer spill,
+// more leave too few warps; eight elements a lane took 108 us, staging through shared
+// memory by bulk copies 140 us, one-shot CTAs with the loads in front 119 us).
+// The codes' scales stay out of the arithmetic (g = sg g', u = su u' with the raw codes' values
+// g', u'; the factors sg, su, w meet once per tile):
+//   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + (a sg)(1 - s),  x = dy u'
+//   d gate = x slope (w su),  d up = dy a (w sg),  y = a u' (w sg su),  d w += x a (sg su).
 #include "abi_checks.h"
 #include "common.cuh"
 #include "launch.h"
@@ -20,7 +28,6 @@
 namespace fp8q {
 namespace {
 
-constexpr int kTilesPerCta = 32;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 struct BwdIn {
@@ -44,140 +51,197 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+// Pairs of fp32, one instruction each.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 make2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
   return r;
 }
-// Four codes -> fp32, before the scale.
-__device__ __forceinline__ void decode4(uint32_t c, float* v) {
-  const uint32_t lo = cvt_f16x2_e4m3x2(c), hi = cvt_f16x2_e4m3x2(c >> 16);
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[0]), "=f"(v[1]) : "r"(lo));
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2]), "=f"(v[3]) : "r"(hi));
+__device__ __forceinline__ void split2(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(F2 x) {
+  float a, b;
+  split2(x, a, b);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Two codes (in the low or high half of c) -> fp32, before the scale.
+__device__ __forceinline__ F2 decode2(uint32_t c) {
+  const uint32_t h = cvt_f16x2_e4m3x2(c);
+  float x, y;
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(x), "=f"(y) : "r"(h));
+  return make2(x, y);
 }
 // 2^(byte - 127); byte 0 is 2^-127, a subnormal.
 __device__ __forceinline__ float scale_of(uint32_t byte) {
   return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
 }
+// tile_exponent of a finite amax >= 0, shorter: adding 0x1FFFFF carries into the exponent
+// field exactly when the mantissa exceeds 1.75 (the 0x600000 of the rule), and whatever is
+// subnormal lies far below the clamp.
+__device__ __forceinline__ int quick_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  return b == 0u ? 0 : max((int)((b + 0x1FFFFFu) >> 23) - 135, -127);
+}
+// max(|a|, |b|, |c|) in one instruction.
+__device__ __forceinline__ float max3abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
-// Row-wise quantization of a tile's eight lanes x 16 values.
-__device__ __forceinline__ void quantize_store(float (&v)[16], uint8_t* q, uint8_t* sf, int64_t at, int64_t tile,
-                                               int sub, bool live) {
-  float amax = 0.0f;
+// Row-wise quantization of v * factor over a tile's eight lanes x 16 values.  The factor is
+// applied to the maximum, and together with 2^-e to the values.
+__device__ __forceinline__ void quantize_store(const F2 (&v)[8], float factor, uint8_t* q, uint8_t* sf, int64_t at,
+                                               int64_t tile, int sub, bool live) {
+  float x[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  for (int i = 0; i < 8; ++i) split2(v[i], x[2 * i], x[2 * i + 1]);
+  float amax = fmaxf(max3abs(max3abs(x[0], x[1], x[2]), max3abs(x[3], x[4], x[5]), max3abs(x[6], x[7], x[8])),
+                     max3abs(max3abs(x[9], x[10], x[11]), max3abs(x[12], x[13], x[14]), x[15]));
 #pragma unroll
   for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-  const int e = tile_exponent(amax);
-  const float s = exp2_neg(e);
+  const int e = quick_exponent(amax * fabsf(factor));
+  const float f = factor * exp2_neg(e);
+  const F2 f2 = make2(f, f);
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = cvt_e4m3x2_f32(v[4 * i] * s, v[4 * i + 1] * s) | (cvt_e4m3x2_f32(v[4 * i + 2] * s, v[4 * i + 3] * s) << 16);
+  for (int i = 0; i < 4; ++i) {
+    float a0, a1, b0, b1;
+    split2(mul2(v[2 * i], f2), a0, a1);
+    split2(mul2(v[2 * i + 1], f2), b0, b1);
+    c[i] = __byte_perm(cvt_e4m3x2_f32(a0, a1), cvt_e4m3x2_f32(b0, b1), 0x5410);
+  }
   if (live) {
     *reinterpret_cast<uint4*>(q + at) = make_uint4(c[0], c[1], c[2], c[3]);
     if (sub == 0) sf[tile] = (uint8_t)(e + 127);
   }
 }
 
+constexpr int kThreads = 128;
+
+// What eight lanes need of one tile.
+struct TileIn {
+  uint4 g, u, d0, d1;
+  uint32_t gs, us;
+};
+
 template <bool Fp8>
-__global__ void __launch_bounds__(256) swiglu_bwd_kernel(BwdIn in, int64_t rows, int tiles, int rows_per_cta,
-                                                         BwdOut out) {
-  __shared__ float part[kTilesPerCta];
+__global__ void __launch_bounds__(kThreads, Fp8 ? 5 : 6) swiglu_bwd_kernel(BwdIn in, int64_t rows, int tiles,
+                                                                                  int per_warp, BwdOut out) {
   pdl_wait_for(in.gq, in.gsf, in.uq, in.usf, in.dy, in.w);
   pdl_trigger();
-  const int sub = threadIdx.x & 7, slot = threadIdx.x >> 3;
-  const int width = min(tiles, kTilesPerCta);  // tile slots per row
-  const int rl = slot / width;                 // row within the CTA (>= rows_per_cta: idle lanes)
-  const int64_t row = (int64_t)blockIdx.x * rows_per_cta + rl;
-  const bool row_ok = rl < rows_per_cta && row < rows;
+  const int lane = threadIdx.x & 31, sub = lane & 7, group = lane >> 3;
+  const int lanes = 32 / per_warp, step = 4 / per_warp;  // lanes and tiles of a pass per row
+  const int64_t row = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * per_warp + group / step;
+  const bool row_ok = row < rows;
   const float w = row_ok && in.w != nullptr ? ld_g(in.w + row) : 1.0f;
-  float sum = 0.0f;
-  for (int t0 = 0; t0 < tiles; t0 += kTilesPerCta) {  // one step unless a row has more than 32 tiles
-    const int t = t0 + slot - rl * width;
-    const bool live = row_ok && t < tiles;
-    const int64_t tile = row * tiles + t;
-    const int64_t at = tile * 128 + sub * 16;
-    uint4 gc = make_uint4(0u, 0u, 0u, 0u), uc = gc, d0 = gc, d1 = gc;
-    uint32_t gs = 127, us = 127;
-    if (live) {
-      gc = ld_stream(reinterpret_cast<const uint4*>(in.gq + at));
-      uc = ld_stream(reinterpret_cast<const uint4*>(in.uq + at));
-      d0 = ld_stream(reinterpret_cast<const uint4*>(in.dy + at));
-      d1 = ld_stream(reinterpret_cast<const uint4*>(in.dy + at + 8));
-      gs = ld_g(in.gsf + tile);
-      us = ld_g(in.usf + tile);
+  const int64_t tile0 = row * tiles;
+  auto load = [&](int t) {
+    TileIn v;
+    v.g = v.u = v.d0 = v.d1 = make_uint4(0u, 0u, 0u, 0u);
+    v.gs = v.us = 127u;
+    if (row_ok && t < tiles) {
+      const int64_t at = (tile0 + t) * 128 + sub * 16;
+      v.g = ld_stream(reinterpret_cast<const uint4*>(in.gq + at));
+      v.u = ld_stream(reinterpret_cast<const uint4*>(in.uq + at));
+      v.d0 = ld_stream(reinterpret_cast<const uint4*>(in.dy + at));
+      v.d1 = ld_stream(reinterpret_cast<const uint4*>(in.dy + at + 8));
+      v.gs = ld_g(in.gsf + tile0 + t);
+      v.us = ld_g(in.usf + tile0 + t);
     }
+    return v;
+  };
+  float sum = 0.0f;
+  TileIn next = load(group % step);
+  for (int t0 = 0; t0 < tiles; t0 += step) {
+    const int t = t0 + group % step;
+    const bool live = row_ok && t < tiles;
+    const TileIn v = next;
+    if (t0 + step < tiles) next = load(t + step);
+    const int64_t tile = tile0 + t;
+    const int64_t at = tile * 128 + sub * 16;
+    const uint4 gc = v.g, uc = v.u, d0 = v.d0, d1 = v.d1;
+    const uint32_t gs = v.gs, us = v.us;
     const float sg = scale_of(gs), su = scale_of(us);
     const uint32_t gw[4] = {gc.x, gc.y, gc.z, gc.w}, uw[4] = {uc.x, uc.y, uc.z, uc.w};
     const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-    float dg[16], du[16], y[16];
+    // exp(-g) by the hardware base-2 exponential: its argument is off by at most |g| * 2^-23,
+    // far below the outputs' 8 bits.  An exponential of +inf gives s = 0.
+    const F2 k2 = make2(sg * -1.44269504f, sg * -1.44269504f), sg2 = make2(sg, sg);
+    const F2 one = make2(1.0f, 1.0f), minus = make2(-1.0f, -1.0f);
+    F2 dg[8], du[8], y[8], dot = make2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float g[4], u[4];
-      decode4(gw[i], g);
-      decode4(uw[i], u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 4 * i + j;
-        const float dyk = __uint_as_float((j & 1) ? dw[k >> 1] & 0xFFFF0000u : dw[k >> 1] << 16);
-        const float gv = g[j] * sg, uv = u[j] * su;
-        // exp(-g) by the hardware base-2 exponential: its argument is off by at most
-        // |g| * 2^-24 * 1.5, far below the outputs' 8 bits; for g > -30 or so s itself
-        // stays within 2^-22.  exp overflowing to +inf gives s = 0.
-        const float s = rcp(1.0f + ex2(gv * -1.44269504f));
-        const float act = gv * s;                                    // silu(g)
-        const float slope = s * __fmaf_rn(gv, 1.0f - s, 1.0f);       // silu'(g)
-        const float dyw = dyk * w;
-        dg[k] = (dyw * slope) * uv;  // slope first: it is 0 where u could overflow the product
-        du[k] = dyw * act;
-        const float yv = act * uv;
-        sum = __fmaf_rn(dyk, yv, sum);
-        if (Fp8) y[k] = yv * w;
-      }
+    for (int k = 0; k < 8; ++k) {
+      const F2 g = decode2(gw[k >> 1] >> (16 * (k & 1))), u = decode2(uw[k >> 1] >> (16 * (k & 1)));
+      const F2 d = make2(__uint_as_float(dw[k] << 16), __uint_as_float(dw[k] & 0xFFFF0000u));
+      float e0, e1;
+      split2(mul2(g, k2), e0, e1);
+      split2(add2(make2(ex2(e0), ex2(e1)), one), e0, e1);
+      const F2 s = make2(rcp(e0), rcp(e1));
+      const F2 act = mul2(g, s);
+      const F2 slope = fma2(mul2(act, sg2), fma2(s, minus, one), s);
+      const F2 x = mul2(d, u);
+      dg[k] = mul2(x, slope);
+      du[k] = mul2(d, act);
+      dot = fma2(x, act, dot);
+      if (Fp8) y[k] = mul2(act, u);
+    }
+    {
+      float a0, a1;
+      split2(dot, a0, a1);
+      sum = __fmaf_rn((a0 + a1) * sg, su, sum);
     }
     if (Fp8) {
-      quantize_store(dg, out.dgq, out.dgsf, at, tile, sub, live);
-      quantize_store(du, out.duq, out.dusf, at, tile, sub, live);
-      if (out.yq != nullptr) quantize_store(y, out.yq, out.ysf, at, tile, sub, live);
+      quantize_store(dg, w * su, out.dgq, out.dgsf, at, tile, sub, live);
+      quantize_store(du, w * sg, out.duq, out.dusf, at, tile, sub, live);
+      if (out.yq != nullptr) quantize_store(y, w * sg * su, out.yq, out.ysf, at, tile, sub, live);
     } else if (live) {
-      uint4 v[4];
-      uint32_t* p = reinterpret_cast<uint32_t*>(v);
+      const F2 fg = make2(w * su, w * su), fu = make2(w * sg, w * sg);
+      uint32_t p[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = pack_bf16(dg[2 * i], dg[2 * i + 1]);
-        p[8 + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
+        p[i] = pack_bf16(mul2(dg[i], fg));
+        p[8 + i] = pack_bf16(mul2(du[i], fu));
       }
-      *reinterpret_cast<uint4*>(out.dg + at) = v[0];
-      *reinterpret_cast<uint4*>(out.dg + at + 8) = v[1];
-      *reinterpret_cast<uint4*>(out.du + at) = v[2];
-      *reinterpret_cast<uint4*>(out.du + at + 8) = v[3];
+      *reinterpret_cast<uint4*>(out.dg + at) = make_uint4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<uint4*>(out.dg + at + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+      *reinterpret_cast<uint4*>(out.du + at) = make_uint4(p[8], p[9], p[10], p[11]);
+      *reinterpret_cast<uint4*>(out.du + at + 8) = make_uint4(p[12], p[13], p[14], p[15]);
     }
   }
   if (out.dw == nullptr) return;  // uniform
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
-  if (sub == 0 && slot < kTilesPerCta) part[slot] = sum;
-  __syncthreads();
-  if ((int)threadIdx.x < rows_per_cta) {
-    const int64_t r = (int64_t)blockIdx.x * rows_per_cta + threadIdx.x;
-    if (r < rows) {
-      float s = 0.0f;
-      for (int t = 0; t < width; ++t) s += part[threadIdx.x * width + t];
-      out.dw[r] = s;
-    }
-  }
+  for (int o = lanes >> 1; o >= 1; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
+  if (row_ok && (lane & (lanes - 1)) == 0) out.dw[row] = sum;
 }
 
 template <bool Fp8>
 fp8q_status launch_bwd(const BwdIn& in, int64_t rows, int64_t cols, const BwdOut& out, cudaStream_t stream) {
   const int tiles = (int)(cols / 128);
-  const int per = tiles >= kTilesPerCta ? 1 : kTilesPerCta / tiles;  // rows per CTA
-  const int width = tiles < kTilesPerCta ? tiles : kTilesPerCta;
-  const unsigned threads = (unsigned)((per * width * 8 + 31) / 32 * 32);
-  const int64_t ctas = (rows + per - 1) / per;
-  return launch_after(swiglu_bwd_kernel<Fp8>, dim3((unsigned)ctas), threads, 0, stream, in, rows, tiles, per, out) ==
-                 cudaSuccess
+  const int per_warp = tiles == 1 ? 4 : tiles == 2 ? 2 : 1;
+  const int64_t per_cta = (int64_t)per_warp * (kThreads / 32);
+  return launch_after(swiglu_bwd_kernel<Fp8>, dim3((unsigned)((rows + per_cta - 1) / per_cta)), kThreads, 0, stream, in,
+                      rows, tiles, per_warp, out) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }

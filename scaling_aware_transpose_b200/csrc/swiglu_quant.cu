@@ -41,10 +41,10 @@
 // pass two ahead (crossing into its next block), so one pass of loads is in flight per
 // thread while it computes the other.
 //
-// Training variant (Stash): gate and up are kept for the backward pass as 8-bit codes
-// (fp8q_swiglu_bwd, swiglu_bwd.cu).  They are quantized by the same 1x128 rule from the
-// registers that already hold them, so the two extra outputs cost 2 B of writes and no
-// read per element; y may carry one fp32 factor per row (the routing weight).
+// Training form (swiglu_stash_kernel): gate and up are kept for the backward pass as 8-bit
+// codes (fp8q_swiglu_bwd, swiglu_bwd.cu), quantized by the same 1x128 rule from the registers
+// that already hold them: 2 B of writes and no read per element.  Row-wise only, so a warp
+// walks runs of four tiles that lie contiguously in memory, the next run's loads in flight.
 #include "abi_checks.h"
 #include "common.cuh"
 #include "launch.h"
@@ -220,37 +220,17 @@ __device__ __forceinline__ void load_pass(BlockIn& in, int p, const uint16_t* __
   }
 }
 
-// The training variant's extra operands (all NULL in the plain kernel).
-struct StashArgs {
-  const float* row_weights;  // [rows] or NULL
-  uint8_t *gq, *gsf, *uq, *usf;
-};
-
-// 16 bf16 of one lane of a tile's eight -> 16 codes and the tile's scale byte, by the
-// row-wise rule.
-__device__ __forceinline__ uint4 quantize16(const uint32_t (&w)[8], int& e) {
-  uint32_t m = maxabs_bf16x2(maxabs_bf16x2(maxabs_bf16x2(w[0], w[1]), maxabs_bf16x2(w[2], w[3])),
-                             maxabs_bf16x2(maxabs_bf16x2(w[4], w[5]), maxabs_bf16x2(w[6], w[7])));
-  m = maxabs_bf16x2(m, __byte_perm(m, 0u, 0x1032)) & 0x7FFFu;
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  e = bf16_tile_exponent(m);
-  const float s = exp2_neg(e);
-  return make_uint4(encode4(w[0], w[1], s), encode4(w[2], w[3], s), encode4(w[4], w[5], s), encode4(w[6], w[7], s));
-}
-
-template <bool Stash>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) swiglu_quant_kernel(const uint16_t* __restrict__ gate,
                                                                          const uint16_t* __restrict__ up, int64_t rows,
                                                                          int cols, int nblk,
                                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                                          uint8_t* __restrict__ qt,
-                                                                         uint8_t* __restrict__ sft, StashArgs st) {
+                                                                         uint8_t* __restrict__ sft) {
   __shared__ __align__(16) float silu_tab[kTabPad];
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ __align__(16) uint8_t e_row[128];
   __shared__ int e_max_sh;
-  pdl_wait_for(gate, up, st.row_weights);
+  pdl_wait_for(gate, up);
   pdl_trigger();
   const int tid = threadIdx.x;
   const int ncb = cols >> 7;
@@ -293,23 +273,6 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) swiglu_quant_kernel(cons
 #pragma unroll
       for (int k = 0; k < 8; ++k)  // y = silu(g) * u
         mul2_rn(y[2 * k], y[2 * k + 1], __uint_as_float(uw[k] << 16), __uint_as_float(uw[k] & 0xFFFF0000u));
-      if (Stash) {
-        int eg, eu;
-        const uint4 cg = quantize16(gw, eg), cu = quantize16(uw, eu);
-        if (r < rows) {
-          *reinterpret_cast<uint4*>(st.gq + r * cols + c0 + sub * 16) = cg;
-          *reinterpret_cast<uint4*>(st.uq + r * cols + c0 + sub * 16) = cu;
-          if (sub == 0) {
-            st.gsf[r * ncb + (c0 >> 7)] = (uint8_t)(eg + 127);
-            st.usf[r * ncb + (c0 >> 7)] = (uint8_t)(eu + 127);
-          }
-        }
-        if (st.row_weights != nullptr) {
-          const float w = r < rows ? ld_g(st.row_weights + r) : 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mul2_rn(y[2 * k], y[2 * k + 1], w, w);
-        }
-      }
       float amax;  // finite y: the largest magnitude, by three-input max instructions
       {
         const float a0 = max3abs(y[0], y[1], y[2]), a1 = max3abs(y[3], y[4], y[5]), a2 = max3abs(y[6], y[7], y[8]);
@@ -384,6 +347,119 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) swiglu_quant_kernel(cons
   }
 }
 
+// ------------------------------------------------------------------ training form
+// Eight lanes per tile, 16 elements each; run u of a warp is tiles 4u .. 4u + 3 of the flat
+// sequence of 1x128 tiles.
+struct StashOut {
+  uint8_t *q, *sf, *gq, *gsf, *uq, *usf;
+};
+constexpr int kStashThreads = 256;
+constexpr int kStashCtas = 3;  // an SM: 80 registers a thread
+
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t chunk_amax(const uint32_t (&w)[8]) {  // as bf16 bits, sign clear
+  uint32_t m = maxabs_bf16x2(maxabs_bf16x2(maxabs_bf16x2(w[0], w[1]), maxabs_bf16x2(w[2], w[3])),
+                             maxabs_bf16x2(maxabs_bf16x2(w[4], w[5]), maxabs_bf16x2(w[6], w[7])));
+  return maxabs_bf16x2(m, __byte_perm(m, 0u, 0x1032)) & 0x7FFFu;
+}
+// 16 values times s -> 16 codes.
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], float s) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a0 = v[4 * i], a1 = v[4 * i + 1], b0 = v[4 * i + 2], b1 = v[4 * i + 3];
+    mul2_rn(a0, a1, s, s);
+    mul2_rn(b0, b1, s, s);
+    c[i] = __byte_perm(cvt_e4m3x2_f32(a0, a1), cvt_e4m3x2_f32(b0, b1), 0x5410);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+__global__ void __launch_bounds__(kStashThreads, kStashCtas) swiglu_stash_kernel(const uint16_t* __restrict__ gate,
+                                                                               const uint16_t* __restrict__ up,
+                                                                               const float* __restrict__ row_weights,
+                                                                               int64_t n_tiles, uint32_t tiles_per_row,
+                                                                               StashOut out) {
+  __shared__ __align__(16) float silu_tab[kTabPad];
+  pdl_wait_for(gate, up, row_weights);
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int64_t stride = (int64_t)gridDim.x * (kStashThreads / 32) * 4;
+  int64_t tile = (((int64_t)blockIdx.x * kStashThreads + threadIdx.x) >> 5) * 4 + (lane >> 3);
+  uint4 ng[2], nu[2];
+  auto load = [&](int64_t t) {
+    if (t < n_tiles) {
+      const int64_t at = t * 128 + sub * 16;
+      ng[0] = ld_stream(reinterpret_cast<const uint4*>(gate + at));
+      ng[1] = ld_stream(reinterpret_cast<const uint4*>(gate + at + 8));
+      nu[0] = ld_stream(reinterpret_cast<const uint4*>(up + at));
+      nu[1] = ld_stream(reinterpret_cast<const uint4*>(up + at + 8));
+    } else {
+      ng[0] = ng[1] = nu[0] = nu[1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load(tile);
+  fill_silu_table(silu_tab);
+  for (; tile - (lane >> 3) < n_tiles; tile += stride) {  // the warp's first tile decides for all
+    const bool live = tile < n_tiles;
+    const uint32_t gw[8] = {ng[0].x, ng[0].y, ng[0].z, ng[0].w, ng[1].x, ng[1].y, ng[1].z, ng[1].w};
+    const uint32_t uw[8] = {nu[0].x, nu[0].y, nu[0].z, nu[0].w, nu[1].x, nu[1].y, nu[1].z, nu[1].w};
+    load(tile + stride);
+    // ---- y, as in swiglu_quant_kernel
+    float y[16];
+    uint32_t acc = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) silu_lookup2(silu_tab, gw[k], y[2 * k], y[2 * k + 1], acc);
+    if (__any_sync(0xFFFFFFFFu, acc != 0u)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y[2 * k] = silu_fix(y[2 * k], gw[k] & 0xFFFFu, __uint_as_float(gw[k] << 16));
+        y[2 * k + 1] = silu_fix(y[2 * k + 1], gw[k] >> 16, __uint_as_float(gw[k] & 0xFFFF0000u));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float lo, hi;
+      unpack2(uw[k], lo, hi);
+      mul2_rn(y[2 * k], y[2 * k + 1], lo, hi);
+    }
+    if (row_weights != nullptr) {
+      const float w = live ? ld_g(row_weights + (uint64_t)tile / tiles_per_row) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mul2_rn(y[2 * k], y[2 * k + 1], w, w);
+    }
+    float amax = fmaxf(max3abs(max3abs(y[0], y[1], y[2]), max3abs(y[3], y[4], y[5]), max3abs(y[6], y[7], y[8])),
+                       max3abs(max3abs(y[9], y[10], y[11]), max3abs(y[12], y[13], y[14]), y[15]));
+    uint32_t mgu = chunk_amax(gw) | (chunk_amax(uw) << 16);  // both maxima in one word
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) {
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      mgu = umax16x2(mgu, __shfl_xor_sync(0xFFFFFFFFu, mgu, o));
+    }
+    const int ey = tile_exponent(amax), eg = bf16_tile_exponent(mgu & 0xFFFFu), eu = bf16_tile_exponent(mgu >> 16);
+    const uint4 cy = encode16(y, exp2_neg(ey));
+    const float sg = exp2_neg(eg), su = exp2_neg(eu);
+    const uint4 cg = make_uint4(encode4(gw[0], gw[1], sg), encode4(gw[2], gw[3], sg), encode4(gw[4], gw[5], sg),
+                                encode4(gw[6], gw[7], sg));
+    const uint4 cu = make_uint4(encode4(uw[0], uw[1], su), encode4(uw[2], uw[3], su), encode4(uw[4], uw[5], su),
+                                encode4(uw[6], uw[7], su));
+    if (live) {
+      const int64_t at = tile * 128 + sub * 16;
+      *reinterpret_cast<uint4*>(out.q + at) = cy;
+      *reinterpret_cast<uint4*>(out.gq + at) = cg;
+      *reinterpret_cast<uint4*>(out.uq + at) = cu;
+      if (sub == 0) {
+        out.sf[tile] = (uint8_t)(ey + 127);
+        out.gsf[tile] = (uint8_t)(eg + 127);
+        out.usf[tile] = (uint8_t)(eu + 127);
+      }
+    }
+  }
+}
+
 // Test hooks: the device exp and SwiGLU spec on raw inputs, for cross-checks against the
 // CPU implementation of the same spec.  exp over the fp32 bit patterns first..first+n-1.
 __global__ void exp_spec_range_kernel(uint32_t first, int64_t n, float* __restrict__ out) {
@@ -422,28 +498,17 @@ __global__ void __launch_bounds__(kThreads) silu_table_kernel(const uint32_t* __
 
 }  // namespace
 
-namespace {
-
-fp8q_status launch_swiglu(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
-                          uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, bool stash, const StashArgs& st,
-                          cudaStream_t stream) {
+fp8q_status launch_swiglu_quant(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
+                                uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, cudaStream_t stream) {
   if (rows == 0 || cols == 0) return FP8Q_OK;
   const int64_t nblk = (rows + 127) / 128 * (cols / 128);
   if (nblk > 0x7FFFFFFF - 0x10000) return FP8Q_ERR_SHAPE;  // block indices are int32
   const int64_t slots = (int64_t)dev.num_sms * kMinBlocks;
   const int64_t grid = nblk < slots ? nblk : slots;
-  return launch_after(stash ? swiglu_quant_kernel<true> : swiglu_quant_kernel<false>, dim3((unsigned)grid), kThreads, 0,
-                      stream, static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(up), rows, (int)cols,
-                      (int)nblk, q, sf, qt, sft, st) == cudaSuccess
+  return launch_after(swiglu_quant_kernel, dim3((unsigned)grid), kThreads, 0, stream, static_cast<const uint16_t*>(gate),
+                      static_cast<const uint16_t*>(up), rows, (int)cols, (int)nblk, q, sf, qt, sft) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
-}
-
-}  // namespace
-
-fp8q_status launch_swiglu_quant(const DeviceInfo& dev, const void* gate, const void* up, int64_t rows, int64_t cols,
-                                uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft, cudaStream_t stream) {
-  return launch_swiglu(dev, gate, up, rows, cols, q, sf, qt, sft, false, StashArgs{}, stream);
 }
 
 fp8q_status launch_debug_exp_spec_range(uint32_t first, int64_t n, float* out, cudaStream_t stream) {
@@ -469,19 +534,22 @@ fp8q_status launch_debug_silu_bf16(const void* g, int64_t n, float* y, cudaStrea
 using namespace fp8q;
 
 extern "C" fp8q_status fp8q_swiglu_quant_stash(const void* gate, const void* up, const float* row_weights, int64_t rows,
-                                               int64_t cols, uint8_t* q, uint8_t* sf, uint8_t* qt, uint8_t* sft,
-                                               uint8_t* gq, uint8_t* gsf, uint8_t* uq, uint8_t* usf,
-                                               fp8q_stream_t stream) {
+                                               int64_t cols, uint8_t* q, uint8_t* sf, uint8_t* gq, uint8_t* gsf,
+                                               uint8_t* uq, uint8_t* usf, fp8q_stream_t stream) {
   if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxInt32 || cols > kMaxInt32) return FP8Q_ERR_SHAPE;
-  if ((qt == nullptr) != (sft == nullptr)) return FP8Q_ERR_ARG;
-  if (qt && rows % 128) return FP8Q_ERR_SHAPE;
   if (rows == 0 || cols == 0) return FP8Q_OK;
   if (!gate || !up || !q || !sf || !gq || !gsf || !uq || !usf) return FP8Q_ERR_NULL;
   if (!aligned_to(gate, 16) || !aligned_to(up, 16) || !aligned_to(q, 16) || !aligned_to(gq, 16) ||
-      !aligned_to(uq, 16) || !aligned_to(qt, 4) || !aligned_to(row_weights, 4))
+      !aligned_to(uq, 16) || !aligned_to(row_weights, 4))
     return FP8Q_ERR_ALIGN;
   DeviceInfo dev;
   if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
-  return launch_swiglu(dev, gate, up, rows, cols, q, sf, qt, sft, true, StashArgs{row_weights, gq, gsf, uq, usf},
-                       to_stream(stream));
+  const int64_t n_tiles = rows * (cols / 128);
+  const int64_t per_cta = kStashThreads / 32 * 4;
+  const int64_t need = (n_tiles + per_cta - 1) / per_cta, most = (int64_t)dev.num_sms * kStashCtas;
+  return launch_after(swiglu_stash_kernel, dim3((unsigned)(need < most ? need : most)), kStashThreads, 0, to_stream(stream),
+                      static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(up), row_weights, n_tiles,
+                      (uint32_t)(cols / 128), StashOut{q, sf, gq, gsf, uq, usf}) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
 }

@@ -226,14 +226,14 @@ def permute_row_weights(weights, row_id_map, rows: int):
 
 
 # ---------------------------------------------------------------- 8-bit SwiGLU checkpoints
-def fp8q_swiglu_quant_stash(gate, up, row_weights, rows: int, cols: int, q, sf, qt, sft, gq, gsf, uq, usf,
+def fp8q_swiglu_quant_stash(gate, up, row_weights, rows: int, cols: int, q, sf, gq, gsf, uq, usf,
                             stream=None) -> None:
     import torch
     bf16, u8, dev, n, t = torch.bfloat16, torch.uint8, _device(), rows * cols, rows * (cols // 128)
     _check(lib().fp8q_swiglu_quant_stash(
         _in(gate, "gate", bf16, n, dev), _in(up, "up", bf16, n, dev),
         _in(row_weights, "row_weights", torch.float32, rows, dev), rows, cols, _in(q, "q", u8, n, dev),
-        _in(sf, "sf", u8, t, dev), _in(qt, "qt", u8, n, dev), _in(sft, "sft", u8, t, dev), _in(gq, "gq", u8, n, dev),
+        _in(sf, "sf", u8, t, dev), _in(gq, "gq", u8, n, dev),
         _in(gsf, "gsf", u8, t, dev), _in(uq, "uq", u8, n, dev), _in(usf, "usf", u8, t, dev), _raw_stream(stream, dev)),
         "fp8q_swiglu_quant_stash")
 
@@ -290,7 +290,7 @@ def swiglu_quant_stash(gate, up, row_weights=None):
     q, sf = _pair(rows, cols, device)
     gq, gsf, uq, usf = (torch.empty_like(t) for t in (q, sf, q, sf))
     _check(lib().fp8q_swiglu_quant_stash(
-        *ins, rows, cols, q.data_ptr(), sf.data_ptr(), None, None, gq.data_ptr(), gsf.data_ptr(), uq.data_ptr(),
+        *ins, rows, cols, q.data_ptr(), sf.data_ptr(), gq.data_ptr(), gsf.data_ptr(), uq.data_ptr(),
         usf.data_ptr(), _raw_stream(None, dev)), "fp8q_swiglu_quant_stash")
     return q, sf, gq, gsf, uq, usf
 

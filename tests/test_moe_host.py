@@ -84,16 +84,14 @@ def test_reference_gradient_against_differences(sigmoid, renorm):
 
 
 def test_swiglu_stash_refusals(L):
-    def f(g=A, u=A, w=None, rows=128, cols=256, q=A, sf=A, qt=None, sft=None, gq=A, gsf=A, uq=A, usf=A):
-        return L.fp8q_swiglu_quant_stash(g, u, w, rows, cols, q, sf, qt, sft, gq, gsf, uq, usf, None)
+    def f(g=A, u=A, w=None, rows=128, cols=256, q=A, sf=A, gq=A, gsf=A, uq=A, usf=A):
+        return L.fp8q_swiglu_quant_stash(g, u, w, rows, cols, q, sf, gq, gsf, uq, usf, None)
 
-    for kw in (dict(rows=-1), dict(cols=100), dict(rows=1 << 31), dict(rows=100, qt=A, sft=A)):
+    for kw in (dict(rows=-1), dict(cols=100), dict(rows=1 << 31)):
         assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
-    for kw in (dict(qt=A), dict(sft=A)):
-        assert f(**kw) == sat.FP8Q_ERR_ARG, kw
     for k in ("g", "u", "q", "sf", "gq", "gsf", "uq", "usf"):
         assert f(**{k: None}) == sat.FP8Q_ERR_NULL, k
-    for kw in (dict(g=M8), dict(u=M8), dict(gq=M8), dict(uq=M8), dict(q=M8), dict(w=M2), dict(qt=M2, sft=A)):
+    for kw in (dict(g=M8), dict(u=M8), dict(gq=M8), dict(uq=M8), dict(q=M8), dict(w=M2)):
         assert f(**kw) == sat.FP8Q_ERR_ALIGN, kw
     assert f(rows=0, g=None) == sat.FP8Q_OK and f(cols=0, gq=None) == sat.FP8Q_OK
 
