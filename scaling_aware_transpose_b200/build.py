@@ -4,7 +4,8 @@
 
 Objects go to _build/ (git-ignored); ptxas register/spill reports to
 _build/ptxas.log.  The shared library lands next to this file so that it travels with
-the source tree.
+the source tree, and beside it _moe_binding.so, the native half of moe.py's helpers
+(csrc/moe_binding.cpp: g++ against torch's headers, linked to the library).
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
+BINDING = os.path.join(PKG, "_moe_binding.so")
+CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
@@ -59,6 +62,28 @@ def _compile(src):
     return obj
 
 
+def _build_binding(force: bool) -> None:
+    src = os.path.join(CSRC, "moe_binding.cpp")
+    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "fp8q.h")])):
+        return
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_moe_binding",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(CUDA, "include"), "-isystem", sysconfig.get_paths()["include"],
+           src, "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python", "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -72,6 +97,7 @@ def build(force: bool = False) -> str:
         subprocess.run([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-Xcompiler", "-fPIC",
                         *objs, "-o", tmp], check=True)
         os.replace(tmp, LIB)
+    _build_binding(force)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as log:
         for o in objs:
             p = o + ".ptxas.txt"
