@@ -43,6 +43,7 @@ constexpr int kThreads = 32 * kWarps;
 // CTAs that 148 SMs hold at once: four an SM (64 registers a thread) up to 256 experts, two
 // above.  A fixed number, so that the order of the sums is the same wherever it runs.
 constexpr int resident(int vpl) { return vpl <= 8 ? 4 : 2; }
+constexpr int resident_bwd(int vpl) { return vpl <= 2 ? 5 : resident(vpl); }
 constexpr int max_blocks(int experts) { return 148 * (experts <= 256 ? resident(8) : resident(16)); }
 constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopk = 64;
@@ -224,10 +225,14 @@ __device__ __forceinline__ void pick_all(const T* __restrict__ row, const float*
       m_lo = __reduce_max_sync(kAll, b);
     }
     uint32_t e = 0xFFFFu;
+    if (VPL == 1) {  // the lowest lane is the lowest id
+      e = __ffs(__ballot_sync(kAll, key[0] == m && (MODE != kSigmoidBias || key_lo[0] == m_lo))) - 1;
+    } else {
 #pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = expert_of<VPL>(lane, i);
-    e = __reduce_min_sync(kAll, e);
+      for (int i = VPL - 1; i >= 0; --i)
+        if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = expert_of<VPL>(lane, i);
+      e = __reduce_min_sync(kAll, e);
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (e == (uint32_t)expert_of<VPL>(lane, i)) key[i] = 0u;
@@ -500,9 +505,17 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int
     __syncwarp();
     cluster_sync();
     if (rank == 0 && wid == 0) {
-      for (uint32_t r = 1; r < size; ++r) {
-        s += ld_cluster_f64(smem_u32(&sum_sh[0][lane]), r);
-        n += ld_cluster_s32(smem_u32(&cnt_sh[0][lane]), r);
+      double ps[kFinishCluster];
+      int pn[kFinishCluster];
+#pragma unroll
+      for (uint32_t r = 1; r < kFinishCluster; ++r) {  // all on their way, then added in rank order
+        ps[r] = r < size ? ld_cluster_f64(smem_u32(&sum_sh[0][lane]), r) : 0.0;
+        pn[r] = r < size ? ld_cluster_s32(smem_u32(&cnt_sh[0][lane]), r) : 0;
+      }
+#pragma unroll
+      for (uint32_t r = 1; r < kFinishCluster; ++r) {
+        s += ps[r];
+        n += pn[r];
       }
     }
     __syncwarp();
@@ -512,19 +525,25 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int
   if (e < E) {
     counts[e] = n;
     prob_sums[e] = (float)s;
-    __threadfence();
   }
-  __syncwarp();
-  if (lane == 0) last = atomicAdd(ws, 1u) == gridDim.x / size - 1;
-  __syncwarp();
-  if (!last) return;
-  __threadfence();
   double dot = 0.0;
   long long c = 0;
-  for (int i = lane; i < E; i += 32) {
-    const int32_t ci = __ldcg(counts + i);
-    dot += (double)ci * (double)__ldcg(prob_sums + i);
-    c += ci;
+  if (E <= 32) {  // one cluster: everything is here
+    c = n;
+    dot = (double)n * (double)(float)s;
+  } else {
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(ws, 1u) == gridDim.x / size - 1;
+    __syncwarp();
+    if (!last) return;
+    __threadfence();
+#pragma unroll 4
+    for (int i = lane; i < E; i += 32) {
+      const int32_t ci = __ldcg(counts + i);
+      dot += (double)ci * (double)__ldcg(prob_sums + i);
+      c += ci;
+    }
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
@@ -536,7 +555,7 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int
 
 // ------------------------------------------------------------------ backward
 template <int VPL, bool SIGMOID, typename T>
-__global__ void __launch_bounds__(kThreads, resident(VPL)) router_bwd_kernel(const T* __restrict__ logits,
+__global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel(const T* __restrict__ logits,
                                                               const uint8_t* __restrict__ mask, RouterArgs a,
                                                               const int32_t* __restrict__ topk_idx,
                                                               const float* __restrict__ grad_weights,
@@ -816,8 +835,10 @@ template <int VPL, typename T>
 cudaError_t launch_bwd(bool sigmoid, const T* logits, const RouterArgs& a, const BwdPtrs& p, T* grad, int* status,
                        cudaStream_t st) {
   auto k = sigmoid ? router_bwd_kernel<VPL, true, T> : router_bwd_kernel<VPL, false, T>;
+  const int64_t need = (a.tokens + kWarps - 1) / kWarps, most = 148 * resident_bwd(VPL);
+  const int64_t blocks = need < most ? need : most;
   const size_t smem = (size_t)(kWarps + 1) * ((a.E + 3) & ~3) * sizeof(float);  // at most 36 KB
-  return launch_after(k, dim3((unsigned)router_blocks(a.tokens, a.E)), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
+  return launch_after(k, dim3((unsigned)blocks), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
                       p.map, p.rows, p.counts, p.loss_coef, p.grad_loss, grad, status);
 }
 
