@@ -11,10 +11,10 @@
 //   warp 0     TMA loads of the A and B codes; every fourth stage, bulk copies of the scale
 //              tiles, which the quantizers store in the order the tensor core reads;
 //   warp 1     four MMAs of 64 elements per stage and a commit that frees it;
-//   warps 2-5  scales: shared memory -> registers -> tensor memory, each warp its quarter of
-//              the lanes.  (tcgen05.cp from the MMA thread took turns with the MMAs: 36 ns a
+//   warps 2-9  scales: shared memory -> registers -> tensor memory, each warp its quarter of
+//              the lanes, two warps a quarter taking turns.  (tcgen05.cp from the MMA thread took turns with the MMAs: 36 ns a
 //              512-byte tile, and as much again for each change from one to the other.)
-//   warps 6-9  the epilogue: tensor memory -> registers -> BF16 -> global.
+//   warps 10-13  the epilogue: tensor memory -> registers -> BF16 -> global.
 // Scale columns in tensor memory belong to the stage: they are rewritten only after the
 // stage's MMAs have completed.
 //
@@ -39,10 +39,11 @@ namespace {
 constexpr int kBM = 128;
 constexpr int kBK = 256;          // elements of k per stage
 constexpr int kRowBytes = kBK / 2;
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
 constexpr int kSfSteps = 4;       // stages per slot of scale tiles
 constexpr int kSfSlots = 2;
 constexpr int kTmemCols = 512;
+constexpr int kPitch = 8;         // words of a staged row piece (16 columns)
 
 template <int BN, int STAGES, int ACC>
 struct Cfg {
@@ -88,6 +89,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
+// The same by one CTA of a pair: the barrier may lie in the other CTA.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -103,6 +115,15 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, 
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                                 uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
@@ -131,10 +152,11 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-// Instruction descriptor of kind::mxf4: E2M1 operands, UE8M0 scales, M = 128, K = 64; the
-// scale ids (bits 4-5 of B, 29-30 of A) pick the half of each 4-byte scale word.
-__device__ __forceinline__ constexpr uint32_t idesc_mxf4(int n, uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (sf_id << 29);
+// Instruction descriptor of kind::mxf4: E2M1 operands, UE8M0 scales, M = 128 or 256, K = 64;
+// the scale ids (bits 4-5 of B, 29-30 of A) pick the half of each 4-byte scale word.
+__device__ __forceinline__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27) |
+         (sf_id << 29);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -167,6 +189,59 @@ __device__ __forceinline__ bool wait_or_record(uint64_t* bar, uint32_t parity, i
   return false;
 }
 
+// One epilogue warp: 32 rows (row0 + lane) x BN columns of the accumulator at `tmem` to BF16
+// rows of out below row_end and columns below n.  `read` is called once the accumulator has
+// been read to the end.
+template <int BN, typename Read>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, uint32_t tmem, int64_t row0, int64_t row_end, int64_t col,
+                                           bool vec, int lane, uint32_t* staging, Read read) {
+  const int64_t r = row0 + lane;
+  uint16_t* dst = a.out + r * a.n + col;
+  const int left = (int)min((int64_t)BN, a.n - col);  // columns of this tile that exist
+  constexpr int kPart = BN < 128 ? BN : 128;          // columns packed in registers at a time
+#pragma unroll 1
+  for (int h = 0; h < BN; h += kPart) {
+    uint32_t p[kPart / 2];
+#pragma unroll
+    for (int c = 0; c < kPart; c += 32) {
+      uint32_t v[32];
+      tc_load32(v, tmem + h + c);
+      tc_wait_load();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[c / 2 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+    if (h + kPart == BN) read();  // the next tile's MMAs may overwrite it
+    if (vec) {
+      if (r < row_end) {
+#pragma unroll
+        for (int c = 0; c < kPart; c += 8)
+          if (h + c < left)
+            *reinterpret_cast<uint4*>(dst + h + c) = make_uint4(p[c / 2], p[c / 2 + 1], p[c / 2 + 2], p[c / 2 + 3]);
+      }
+    } else {
+      // Rows that do not start on 16 bytes: 16 columns at a time through shared memory, so
+      // that half a warp stores 16 neighbouring elements of a row (each lane storing its own
+      // row element by element took 2.5 times as long over the whole product).
+      uint32_t* mine = staging + lane * kPitch;
+      const uint16_t* all = reinterpret_cast<const uint16_t*>(staging);
+      const int rows_here = (int)max((int64_t)0, min((int64_t)32, row_end - row0));
+      uint16_t* base = a.out + row0 * a.n + col + h;
+#pragma unroll
+      for (int c = 0; c < kPart; c += 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine[i] = p[c / 2 + i];
+        __syncwarp();
+        const int x = c + (lane & 15);
+        if (h + x < left) {
+#pragma unroll 4
+          for (int i = lane >> 4; i < rows_here; i += 2) base[i * a.n + x] = all[i * 2 * kPitch + (lane & 15)];
+        }
+        __syncwarp();
+      }
+    }
+  }
+}
+
 template <int BN, int STAGES, int ACC, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -175,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], scaled[STAGES], sf_full[kSfSlots], sf_empty[kSfSlots];
   __shared__ uint64_t acc_full[C::kAcc], acc_empty[C::kAcc], drain;
-  __shared__ uint32_t tmem_sh, odd_rows[4][32 * 9];
+  __shared__ uint32_t tmem_sh, odd_rows[4][32 * kPitch];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -186,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSfSlots; ++s) {
       mbar_init(&sf_full[s], 1);
-      mbar_init(&sf_empty[s], 4);
+      mbar_init(&sf_empty[s], 8);
     }
     for (int s = 0; s < C::kAcc; ++s) {
       mbar_init(&acc_full[s], 1);
@@ -315,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h)  // 64 codes: 32 bytes, two scales of a row's four-byte word
             if (h < 2 || 2 * (j0 + j) + 1 < k128)
-              tc_mma_mxf4(d, da + 2 * h, db + 2 * h, idesc_mxf4(BN, 2 * (h & 1)), tm_a + 4 * (h >> 1),
+              tc_mma_mxf4(d, da + 2 * h, db + 2 * h, idesc_mxf4(kBM, BN, 2 * (h & 1)), tm_a + 4 * (h >> 1),
                           tm_b + 4 * (h >> 1) * C::kAtoms, (uint32_t)(j + h > 0));
           tc_commit(&empty[s]);
           if (j + 1 == steps) tc_commit(&acc_full[acc]);
@@ -337,10 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(&drain, 0u, kWaitTimeoutNs);
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     const int quad = warp & 3;  // the tensor-memory lanes this warp may write
     int s = 0, slot = 0;
-    uint32_t phase = 0, slot_phase = 0;
+    uint32_t phase = 0, slot_phase = 0, turn = warp < 6 ? 0u : 1u;  // two warps a quarter take turns
     bool ok = true;
     for (int64_t t = t0; ok && t < tiles; t += stride) {
       Tile o;
@@ -350,43 +425,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (j % kSfSteps) * 2 * kSfTileBytes + lane * 16;
         if (j % kSfSteps == 0) ok = wait_or_record(&sf_full[slot], slot_phase, a.status);
         if (!ok) break;
-        uint4 v[2 * (1 + C::kAtoms)];
+        if (turn == 0) {
+          uint4 v[2 * (1 + C::kAtoms)];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i <= C::kAtoms; ++i)
-            v[c * (1 + C::kAtoms) + i] = *reinterpret_cast<const uint4*>(sf + i * C::kSfRun + c * kSfTileBytes);
-        if (BN < 128) {
-          // A B tile narrower than a scale tile starts inside it (32 rows per word): its first
-          // word goes to the first column, whose address stays a multiple of four.
-          const uint32_t first = (uint32_t)(o.b_row & 127) >> 5;
+            for (int i = 0; i <= C::kAtoms; ++i)
+              v[c * (1 + C::kAtoms) + i] = *reinterpret_cast<const uint4*>(sf + i * C::kSfRun + c * kSfTileBytes);
+          if (BN < 128) {
+            // A B tile narrower than a scale tile starts inside it (32 rows per word): its first
+            // word goes to the first column, whose address stays a multiple of four.
+            const uint32_t first = (uint32_t)(o.b_row & 127) >> 5;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint4& w = v[2 * c + 1];
+              if (first & 2) w = make_uint4(w.z, w.w, w.z, w.w);
+              if (first & 1) w.x = w.y;  // (32 rows: one word)
+            }
+          }
+          // A filled stage was free before: so are its scale columns.
+          ok = wait_or_record(&full[s], phase, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + C::kAcc * BN + s * C::kSfCols;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint4& w = v[2 * c + 1];
-            if (first & 2) w = make_uint4(w.z, w.w, w.z, w.w);
-            if (first & 1) w.x = w.y;  // (32 rows: one word)
+            tc_store4(tm + 4 * c, v[c * (1 + C::kAtoms)]);
+#pragma unroll
+            for (int i = 0; i < C::kAtoms; ++i)
+              tc_store4(tm + C::kSfaCols + 4 * (c * C::kAtoms + i), v[c * (1 + C::kAtoms) + 1 + i]);
           }
+          tc_wait_store();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scaled[s]);
         }
-        // A filled stage was free before: so are its scale columns.
-        ok = wait_or_record(&full[s], phase, a.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + C::kAcc * BN + s * C::kSfCols;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tc_store4(tm + 4 * c, v[c * (1 + C::kAtoms)]);
-#pragma unroll
-          for (int i = 0; i < C::kAtoms; ++i)
-            tc_store4(tm + C::kSfaCols + 4 * (c * C::kAtoms + i), v[c * (1 + C::kAtoms) + 1 + i]);
-        }
-        tc_wait_store();
-        tc_fence_before();
-        __syncwarp();
+        turn ^= 1u;
         const bool slot_done = (j + 1) % kSfSteps == 0 || j + 1 == steps;
-        if (lane == 0) {
-          mbar_arrive(&scaled[s]);
-          if (slot_done) mbar_arrive(&sf_empty[slot]);
-        }
+        if (slot_done && lane == 0) mbar_arrive(&sf_empty[slot]);
         if (slot_done && ++slot == kSfSlots) {
           slot = 0;
           slot_phase ^= 1u;
@@ -425,54 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         break;
       }
-      uint16_t* dst = a.out + r * a.n + o.col;
-      const int left = (int)min((int64_t)BN, a.n - o.col);  // columns of this tile that exist
-      constexpr int kPart = BN < 128 ? BN : 128;  // columns packed in registers at a time
-#pragma unroll 1
-      for (int h = 0; h < BN; h += kPart) {
-        uint32_t p[kPart / 2];
-#pragma unroll
-        for (int c = 0; c < kPart; c += 32) {
-          uint32_t v[32];
-          tc_load32(v, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN + h + c);
-          tc_wait_load();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p[c / 2 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        }
-        if (h + kPart == BN) {  // read to the end: the next tile's MMAs may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[acc]);
-        }
-        if (vec) {
-          if (r < rows) {
-#pragma unroll
-            for (int c = 0; c < kPart; c += 8)
-              if (h + c < left)
-                *reinterpret_cast<uint4*>(dst + h + c) = make_uint4(p[c / 2], p[c / 2 + 1], p[c / 2 + 2], p[c / 2 + 3]);
-          }
-        } else {
-          // Rows that do not start on 16 bytes: 16 columns at a time through shared memory, so
-          // that half a warp stores 16 neighbouring elements of a row (each lane storing its
-          // own row element by element took 2.5 times as long over the whole product).
-          uint32_t* mine = odd_rows[quad] + lane * 9;
-          const uint16_t* all = reinterpret_cast<const uint16_t*>(odd_rows[quad]);
-          const int rows_here = (int)max((int64_t)0, min((int64_t)32, rows - (o.row + quad * 32)));
-          uint16_t* base = a.out + (o.row + quad * 32) * a.n + o.col + h;
-#pragma unroll
-          for (int c = 0; c < kPart; c += 16) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mine[i] = p[c / 2 + i];
-            __syncwarp();
-            const int col = c + (lane & 15);
-            if (h + col < left) {
-#pragma unroll 4
-              for (int i = lane >> 4; i < rows_here; i += 2) base[i * a.n + col] = all[i * 18 + (lane & 15)];
-            }
-            __syncwarp();
-          }
-        }
-      }
+      store_tile<BN>(a, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN, o.row + quad * 32, rows, o.col, vec, lane,
+                     odd_rows[quad], [&] {
+                       tc_fence_before();
+                       __syncwarp();
+                       if (lane == 0) mbar_arrive(&acc_empty[acc]);
+                     });
       if (++acc == C::kAcc) {
         acc = 0;
         acc_phase ^= 1u;
@@ -573,21 +607,377 @@ fp8q_status launch_matmul(const DeviceInfo& dev, const uint8_t* aq, const uint8_
              : FP8Q_ERR_CUDA;
 }
 
-// Which tile width, and how many CTAs share a tile's k.  Modelled time in ns; each CTA runs
-// `steps` stages for each of its tiles.  Measured, an SM at a time and then all of them:
-//   a stage takes 290 / 300 / 345 / 500 ns at 32 / 64 / 128 / 256 columns (the wait, four MMAs
-//   of at least 50 ns, and with every SM busy the shared-memory traffic), so the widest tile
-//   is the fastest per output (4.5 PFLOP/s at 8192x4096x7168; 3.4 at 128 columns, 1.9 at 64)
-//   as long as its tiles fill the SMs;
+// ------------------------------------------------------------------ CTA pairs
+// Large products: two CTAs of a cluster share one tile of 256 x 256.  Each loads its 128 rows
+// of A and of B (half the B bytes of a CTA alone) and holds 128 rows of the accumulator; the
+// first one's MMAs (cta_group::2, M = 256) read both.  A CTA alone at 128 x 256 moves 48 KB of
+// codes into shared memory and 48 KB out per stage, more than the 128 bytes a cycle allow
+// under the MMAs; a pair moves 32 KB each way: 475 cycles a stage against 955.  At 8192^3 it
+// runs at 5.2 PFLOP/s for the first milliseconds and at 4.65 under the 1000 W cap, which
+// takes the SM clock to 1.55 GHz (a CTA alone there: 4.25).
+// What the pair exchanges: the copies of both complete on the first CTA's `full`; the second
+// one's scale warps and epilogue arrive on the first one's `scaled` and `acc_empty`; warp 18 of
+// the first CTA passes `empty` and `acc_full`, which the MMAs' commits set, on to the second.
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 608;
+constexpr int kPairMaxGroups = 256;
+constexpr int kPairStageBytes = 2 * kBM * kRowBytes;
+constexpr int kPairSlotBytes = 3 * kSfSteps * 2 * kSfTileBytes;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + kSfSlots * kPairSlotBytes;
+constexpr int kPairSfCols = 24, kPairN = 256;
+static_assert(kPairN + kPairStages * kPairSfCols <= kTmemCols, "tensor memory");
+static_assert(kPairSmem <= 217 * 1024, "shared memory");  // 10 KB more are static
+
+// What crosses between the two CTAs through these barriers is the order of tensor-memory and
+// asynchronous-copy operations, which tcgen05's fences and waits and the copies' completion
+// settle; no ordinary memory is handed over.  So arrivals and waits keep the barriers' default
+// (CTA) scope: at cluster scope each cost several hundred cycles (a stage 1050 ns, not 490).
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+struct PairTile {
+  int64_t row, row_end, col, b_row;
+};
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    mxfp4_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, MatmulArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kPairStages], empty[kPairStages], scaled[kPairStages], sf_full[kSfSlots], sf_empty[kSfSlots];
+  __shared__ uint64_t acc_full, acc_empty, drain;
+  __shared__ uint32_t tmem_sh, odd_rows[8][32 * kPitch];
+  __shared__ int tiles_before[kPairMaxGroups + 1];  // of 256 rows, in the groups before g
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool first = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&scaled[s], 8);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_empty[s], 8);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&acc_empty, 16);
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_sh)),
+                 "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and tensor memory exist
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_wait_for(a.a_sf, a.b_sf, a.offsets, a.out);
+  pdl_trigger();
+
+  const int64_t n_tiles = (a.n + kPairN - 1) / kPairN;
+  int64_t m_tiles = (a.m + 2 * kBM - 1) / (2 * kBM);
+  if (a.offsets != nullptr) {
+    const bool report = blockIdx.x == 0 && threadIdx.x == 0;
+    const int64_t rows = grouped_rows(a.offsets, a.groups, a.m, report ? a.status : nullptr);
+    if (blockIdx.x == 0) validate_groups_cta(a.offsets, a.groups, a.status);
+    if (warp == 0) {  // scan of the groups' tile counts; an inconsistent group has none
+      int run = 0;
+      for (int g0 = 0; g0 < a.groups; g0 += 32) {
+        int c = 0;
+        if (g0 + lane < a.groups) {
+          const int64_t b = ld_g(a.offsets + g0 + lane), e = ld_g(a.offsets + g0 + lane + 1);
+          if (b >= 0 && b <= e && e <= rows && ((b | e) & 127) == 0) c = (int)((e - b + 2 * kBM - 1) / (2 * kBM));
+        }
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (g0 + lane < a.groups) tiles_before[g0 + lane] = run + incl - c;
+        run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      }
+      if (lane == 0) tiles_before[a.groups] = run;
+    }
+    __syncthreads();
+    m_tiles = tiles_before[a.groups];
+  }
+  const int64_t tiles = m_tiles * n_tiles;
+  const int64_t t0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const int k128 = a.k / 128;
+  const int steps = (a.k + kBK - 1) / kBK;
+  auto locate_pair = [&](int64_t t) {
+    PairTile o;
+    const int64_t tm = t / n_tiles;
+    o.col = t % n_tiles * kPairN;
+    o.b_row = o.col;
+    o.row = tm * 2 * kBM;
+    o.row_end = a.m;
+    if (a.offsets != nullptr) {
+      int lo = 0, hi = a.groups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles_before[mid] <= tm) lo = mid; else hi = mid;
+      }
+      o.row = ld_g(a.offsets + lo) + (tm - tiles_before[lo]) * 2 * kBM;
+      o.row_end = ld_g(a.offsets + lo + 1);
+      o.b_row += lo * a.n;
+    }
+    return o;
+  };
+
+  if (warp == 0) {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    int s = 0, slot = 0;
+    uint32_t phase = 0, slot_phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    const int64_t b_rows = a.offsets ? a.n * a.groups : a.n;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
+      const PairTile o = locate_pair(t);
+      const int64_t row = o.row + rank * kBM;      // this CTA's rows of A and of B
+      const int64_t b_row = o.b_row + rank * kBM;
+      const uint8_t* sfa = a.a_sf + (row >> 7) * k128 * kSfTileBytes;
+      const uint8_t* sfb = a.b_sf + (o.b_row >> 7) * k128 * kSfTileBytes;
+      const int a_atoms = row < a.m ? 1 : 0;  // scale tiles that exist
+      const int b_atoms = (int)min((int64_t)2, (b_rows - o.b_row + 127) >> 7);
+      for (int j = 0; j < steps; ++j) {
+        if (j % kSfSteps == 0) {
+          ok = wait_or_record(&sf_empty[slot], slot_phase ^ 1u, a.status);
+          if (!ok) break;
+          const uint32_t bytes = min(2 * kSfSteps, k128 - 2 * j) * kSfTileBytes;
+          const uint32_t sf = smem + kPairStages * kPairStageBytes + slot * kPairSlotBytes;
+          constexpr uint32_t kRun = kSfSteps * 2 * kSfTileBytes;
+          if (elect_one()) {
+            mbar_expect_tx(&sf_full[slot], (a_atoms + b_atoms) * bytes);
+            if (a_atoms) bulk_load(sf, sfa + (int64_t)j * 2 * kSfTileBytes, bytes, &sf_full[slot]);
+            for (int i = 0; i < b_atoms; ++i)
+              bulk_load(sf + (1 + i) * kRun, sfb + ((int64_t)i * k128 + (int64_t)j * 2) * kSfTileBytes, bytes,
+                        &sf_full[slot]);
+          }
+          __syncwarp();
+          if (++slot == kSfSlots) {
+            slot = 0;
+            slot_phase ^= 1u;
+          }
+        }
+        ok = wait_or_record(&empty[s], phase ^ 1u, a.status);
+        if (!ok) break;
+        const uint32_t base = smem + s * kPairStageBytes;
+        const uint32_t bar = peer_address(smem_u32(&full[s]), 0);
+        if (elect_one()) {
+          if (first) mbar_expect_tx(&full[s], 2 * kPairStageBytes);
+          tma_load_2d_pair(base, &map_a, j * kRowBytes, (int)row, bar);
+          tma_load_2d_pair(base + kBM * kRowBytes, &map_b, j * kRowBytes, (int)b_row, bar);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == kPairStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // Fills end before the CTA does: on the regular path each was consumed (its stage was
+    // freed).  After an expired wait the first CTA's `full` says when both CTAs' copies have
+    // landed; the second CTA then leaves with the cluster barrier below.
+    for (int i = 0; i < kPairStages && issued > 0; ++i, --issued) {
+      if (s == 0) {
+        s = kPairStages;
+        phase ^= 1u;
+      }
+      --s;
+      if (ok) mbar_wait_bounded(&empty[s], phase, kWaitTimeoutNs);
+      else if (first) mbar_wait_bounded(&full[s], phase, kWaitTimeoutNs);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {  // (a slot never filled passes at once)
+      if (slot == 0) {
+        slot = kSfSlots;
+        slot_phase ^= 1u;
+      }
+      --slot;
+      mbar_wait_bounded(&sf_full[slot], slot_phase, kWaitTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (first) {
+      int s = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int64_t t = t0; ok && t < tiles; t += stride) {
+        ok = wait_or_record(&acc_empty, acc_phase ^ 1u, a.status);
+        if (!ok) break;
+        acc_phase ^= 1u;
+        for (int j = 0; j < steps; ++j) {
+          ok = wait_or_record(&scaled[s], phase, a.status);  // the codes have landed, too
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tm_a = tmem + kPairN + s * kPairSfCols, tm_b = tm_a + 8;
+          const uint64_t da = desc_codes(smem + s * kPairStageBytes);
+          const uint64_t db = desc_codes(smem + s * kPairStageBytes + kBM * kRowBytes);
+          if (elect_one()) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (h < 2 || 2 * j + 1 < k128)
+                tc_mma_mxf4_pair(tmem, da + 2 * h, db + 2 * h, idesc_mxf4(2 * kBM, kPairN, 2 * (h & 1)),
+                                 tm_a + 4 * (h >> 1), tm_b + 8 * (h >> 1), (uint32_t)(j + h > 0));
+            tc_commit_pair(&empty[s]);
+            if (j + 1 == steps) tc_commit_pair(&acc_full);
+          }
+          __syncwarp();
+          if (++s == kPairStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        if (elect_one()) tc_commit_pair(&drain);
+        __syncwarp();
+        mbar_wait_bounded(&drain, 0u, kWaitTimeoutNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 10) {
+    const int quad = warp & 3;  // the tensor-memory lanes this warp may write
+    int s = 0, slot = 0;
+    uint32_t phase = 0, slot_phase = 0, turn = warp < 6 ? 0u : 1u;  // two warps a quarter take turns
+    bool ok = true;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
+      for (int j = 0; j < steps; ++j) {
+        const uint8_t* sf = smem_raw + (smem - smem_u32(smem_raw)) + kPairStages * kPairStageBytes + slot * kPairSlotBytes +
+                            (j % kSfSteps) * 2 * kSfTileBytes + lane * 16;
+        if (j % kSfSteps == 0) ok = wait_or_record(&sf_full[slot], slot_phase, a.status);
+        if (!ok) break;
+        if (turn == 0) {
+          uint4 v[6];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              v[c * 3 + i] = *reinterpret_cast<const uint4*>(sf + i * kSfSteps * 2 * kSfTileBytes + c * kSfTileBytes);
+          // A stage filled (the first CTA sees that) or passed on as free: its scale columns are
+          // free in both CTAs.
+          ok = first ? wait_or_record(&full[s], phase, a.status) : wait_or_record(&empty[s], phase ^ 1u, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + kPairN + s * kPairSfCols;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tc_store4(tm + 4 * c, v[c * 3]);
+            tc_store4(tm + 8 + 8 * c, v[c * 3 + 1]);
+            tc_store4(tm + 12 + 8 * c, v[c * 3 + 2]);
+          }
+          tc_wait_store();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(peer_address(smem_u32(&scaled[s]), 0));
+        }
+        turn ^= 1u;
+        const bool slot_done = (j + 1) % kSfSteps == 0 || j + 1 == steps;
+        if (slot_done && lane == 0) mbar_arrive(&sf_empty[slot]);
+        if (slot_done && ++slot == kSfSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+        if (++s == kPairStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 18) {
+    const int quad = warp & 3, half = (warp - 10) >> 2;  // a quarter of the rows, half of the columns
+    uint32_t acc_phase = 0;
+    const bool vec = (a.n & 7) == 0;
+    for (int64_t t = t0; t < tiles; t += stride) {
+      const PairTile o = locate_pair(t);
+      if (!wait_or_record(&acc_full, acc_phase, a.status)) break;
+      acc_phase ^= 1u;
+      tc_fence_after();
+      const int64_t row0 = o.row + rank * kBM + quad * 32;
+      store_tile<kPairN / 2>(a, tmem + ((uint32_t)(quad * 32) << 16) + half * (kPairN / 2), row0, o.row_end,
+                             o.col + half * (kPairN / 2), vec, lane, odd_rows[warp - 10], [&] {
+                               tc_fence_before();
+                               __syncwarp();
+                               if (lane == 0) arrive_at(peer_address(smem_u32(&acc_empty), 0));
+                             });
+    }
+    __syncwarp();
+  } else if (first) {
+    // Passes the commits on to the second CTA.
+    int s = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int64_t t = t0; ok && t < tiles; t += stride) {
+      for (int j = 0; ok && j < steps; ++j) {
+        ok = wait_or_record(&empty[s], phase, a.status);
+        if (ok && lane == 0) arrive_at(peer_address(smem_u32(&empty[s]), 1));
+        __syncwarp();
+        if (++s == kPairStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      ok = wait_or_record(&acc_full, acc_phase, a.status);
+      acc_phase ^= 1u;
+      if (ok && lane == 0) arrive_at(peer_address(smem_u32(&acc_full), 1));
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing of either CTA is in flight to the other
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+  }
+}
+
+fp8q_status launch_pair(const DeviceInfo& dev, const uint8_t* aq, const uint8_t* bq, MatmulArgs a, cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  if (!code_map(&ma, aq, a.m, a.k, kBM) || !code_map(&mb, bq, a.n * a.groups, a.k, kBM)) return FP8Q_ERR_CUDA;
+  static std::atomic<uint64_t> prepared{0};
+  if (!(prepared.load(std::memory_order_relaxed) >> dev.device & 1)) {
+    if (cudaFuncSetAttribute(mxfp4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    prepared.fetch_or(1ull << dev.device, std::memory_order_relaxed);
+  }
+  const int64_t tiles = ((a.m + 2 * kBM - 1) / (2 * kBM) + (a.offsets ? a.groups : 0)) * ((a.n + kPairN - 1) / kPairN);
+  const int64_t pairs = dev.num_sms / 2;
+  return launch_clusters_after(mxfp4_pair_kernel, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), 2u, kPairThreads,
+                               (size_t)kPairSmem, stream, ma, mb, a) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
+}
+
+// Which kernel: a tile width for CTAs alone, and how many of them share a tile's k; or pairs.
+// Modelled time in ns; each CTA runs `steps` stages for each of its tiles.  Measured (an SM at
+// a time, then all of them):
+//   a stage of a CTA alone takes 290 / 300 / 345 / 500 ns at 32 / 64 / 128 / 256 columns (the
+//   wait, four MMAs of at least 50 ns, and with every SM busy the shared-memory traffic), so
+//   the widest tile is the fastest per output as long as its tiles fill the SMs;
 //   a tile's epilogue that no other tile's MMAs cover takes about 4 ns a column;
 //   sharing k saves stages and costs the exchange of the sums: 1.2 us and 0.12 ns for each of
 //   the tile's stored elements (1x4096x7168: 11.3 us unshared at 64 columns, 7.0 us with 4
-//   CTAs at 128; 256x4096x4096: 8.2 us unshared at 64, 9.1 us with 2 at 128).  It is taken
-//   within one wave only, where the clusters are resident together.
+//   CTAs at 128; 256x4096x4096: 7.9 us unshared at 64, 9.1 us with 2 at 128).  It is taken
+//   within one wave only, where the clusters are resident together;
+//   a pair's stage takes 330 ns for twice the rows, its start 3.1 us more than a CTA's alone,
+//   a change of tiles 0.7 us (8192x4096x7168: 96 us against 105 us; 2048x4096x4096: 21.2
+//   against 21.4; 1024x4096x4096: 12.7 against 11.3).  With groups, the last 256 rows of each
+//   may be half empty: pairs are left to groups of 512 rows on average.
 struct Variant {
-  int bn, split;
+  int bn, split;  // bn 0: pairs
 };
-Variant choose(int64_t m, int64_t n, int64_t k, int sms) {
+Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sms) {
   constexpr int kBn[4] = {256, 128, 64, 32};
   constexpr double kStage[4] = {500, 345, 300, 290};
   const int64_t steps = (k + kBK - 1) / kBK;
@@ -605,6 +995,11 @@ Variant choose(int64_t m, int64_t n, int64_t k, int sms) {
         best = {kBn[i], s};
       }
     }
+  }
+  if (!grouped || (groups <= kPairMaxGroups && m >= 512 * (int64_t)groups)) {
+    const int64_t tiles = (m + 2 * kBM - 1) / (2 * kBM) * ((n + kPairN - 1) / kPairN);
+    const double waves = (double)((tiles + sms / 2 - 1) / (sms / 2));
+    if (3100 + waves * ((double)steps * 330 + 700) < least) best = {0, 1};
   }
   return best;
 }
@@ -631,8 +1026,9 @@ extern "C" fp8q_status fp8q_matmul_mxfp4(const uint8_t* aq, const uint8_t* asf, 
   const int a_rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const MatmulArgs a = {asf, bsf, group_offsets, static_cast<uint16_t*>(out), m, n, (int)k, num_groups, a_rows, dev.status};
   cudaStream_t st = to_stream(stream);
-  const Variant v = choose(m, n, k, dev.num_sms);
+  const Variant v = choose(m, n, k, group_offsets != nullptr, num_groups, dev.num_sms);
   switch (v.bn * (v.split > 1 ? -1 : 1)) {
+    case 0: return launch_pair(dev, aq, bq, a, st);
     case 32: return launch_matmul<32, 9, 2, false>(dev, aq, bq, a, 1, st);
     case 64: return launch_matmul<64, 8, 2, false>(dev, aq, bq, a, 1, st);
     case 128: return launch_matmul<128, 6, 2, false>(dev, aq, bq, a, 1, st);

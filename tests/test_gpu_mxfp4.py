@@ -166,6 +166,24 @@ def test_product_large(m, n, k):
     product(m, n, k, 2, m)
 
 
+@pytest.mark.parametrize("m,n,k", [(2, 4821, 128), (130, 2048, 1152), (61, 2467, 3456), (40, 2560, 3456), (5, 67, 1664),
+                                   (128, 200, 3200), (2, 10885, 384), (300, 5120, 640), (2, 5597, 3456), (7, 5600, 3456),
+                                   (2, 2469, 1920), (100, 2472, 1920), (131, 9690, 640), (256, 9728, 896),
+                                   (2, 9735, 4992), (90, 9736, 4992), (2, 4884, 2944), (128, 4888, 2944)])
+def test_product_by_every_tile_width(m, n, k):
+    """Sizes on either side of 16-byte rows for each tile width, alone and with k shared by two
+    or four CTAs (odd numbers of scale tiles among them)."""
+    product(m, n, k, 3, m + n)
+
+
+@pytest.mark.parametrize("m,n,k", [(2048, 4096, 4096), (2001, 4001, 4224), (4096, 2050, 7168), (3300, 3584, 2176),
+                                   (2561, 2560, 8192)])
+def test_product_by_pairs(m, n, k):
+    """Sizes that CTA pairs take: whole 256 x 256 tiles, a second CTA without rows, ragged
+    columns, an odd number of scale tiles."""
+    product(m, n, k, 2, m)
+
+
 def test_product_wide_scales_and_nan():
     product(130, 140, 640, 20)
     aq, asf, a = operand(4, 256, 1)
@@ -211,6 +229,30 @@ def test_grouped(sizes, n):
             near(out[at:at + s], want, tol, f"group {g}")
         at += s
     assert (out[rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("sizes,n,k", [([1408, 0, 1152, 640], 2048, 2304), ([128, 2048, 128, 1664], 1152, 4224),
+                                       ([2560, 0, 0], 2432, 3968)])
+def test_grouped_by_pairs(sizes, n, k):
+    """Groups whose last 256 rows are half full, empty and single-tile groups among large ones."""
+    G, rows = len(sizes), sum(sizes)
+    cap = rows + 300
+    aq, asf, a = operand(cap, k, rows, 2)
+    bq, bsf, b = operand(G * n, k, rows + 1, 2)
+    off = torch.tensor(np.cumsum([0, *sizes]), dtype=torch.int32, device="cuda")
+    out = torch.full((cap, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    sat.matmul_mxfp4(aq, asf, bq, bsf, group_offsets=off, out=out)
+    device_status_ok()
+    at = 0
+    for g, s in enumerate(sizes):
+        if s:
+            want, tol = matmul_bound(a[at:at + s], b[g * n:(g + 1) * n])
+            near(out[at:at + s], want, tol, f"group {g}")
+        at += s
+    assert (out[rows:] == 7.0).all()
+    for bad in ([0, 100, *off.tolist()[2:]], [128, *off.tolist()[1:]], [*off.tolist()[:-1], cap + 84]):
+        sat.matmul_mxfp4(aq, asf, bq, bsf, group_offsets=torch.tensor(bad, dtype=torch.int32, device="cuda"), out=out)
+        assert sat.fp8q_last_device_status() == sat.FP8Q_ERR_SHAPE, bad
 
 
 def test_bad_groups_are_reported_and_skipped():
