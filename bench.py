@@ -72,10 +72,19 @@ def kernel_sources(kind: str):
             "direct_stress": "direct_transpose.cu",
             "permute_fp8": "permute_pad_quant.cu", "ep_pack": "ep_dispatch.cu", "ep_recv": "ep_dispatch.cu",
             "permute_e512": "permute_pad_quant.cu", "permute_e4096": "permute_pad_quant.cu",
-            "unpermute_fp8_k": "unpermute_unpad.cu"}[kind]
+            "unpermute_fp8_k": "unpermute_unpad.cu", "router": "router.cu", "router_wide": "router.cu",
+            "swiglu_stash": "swiglu_quant.cu", "swiglu_bwd": "swiglu_bwd.cu", "swiglu_bwd_quant": "swiglu_bwd.cu",
+            "mxfp4_quantize": "mxfp4_quant.cu", "mxfp4_permute": "mxfp4_quant.cu", "mxfp4_matmul": "mxfp4_matmul.cu",
+            "mxfp4_token": "mxfp4_matmul.cu", "mxfp4_experts": "mxfp4_matmul.cu"}[kind]
     extra = ["permute_common.cuh", "permute_pad_quant.cu"] if kind in ("ep_pack", "ep_recv") else []
     if kind in ("permute", "permute_fp8", "permute_e512", "permute_e4096"):
         extra = ["permute_common.cuh"]
+    if kind.startswith("router"):
+        extra = ["cluster.cuh"]
+    if kind in ("mxfp4_quantize", "mxfp4_permute"):
+        extra = ["mxfp4.cuh", "permute_common.cuh"]
+    if kind in ("mxfp4_matmul", "mxfp4_token", "mxfp4_experts"):
+        extra = ["mxfp4.cuh", "bulk.cuh", "cluster.cuh"]
     return [os.path.join(csrc, main), os.path.join(csrc, "common.cuh")] + [os.path.join(csrc, e) for e in extra]
 
 
@@ -857,6 +866,45 @@ def run_profile(args):
         pq, psf, off, rmap = sat.permute_pad_quant(x, idx, d["num_experts"], 128)
         del x
         calls = {"unpermute_fp8_k": lambda: sat.unpermute_unpad(pq, rmap, K, None, psf)}
+    elif args.profile.startswith("router"):
+        # forward and backward of a training step: the MoE workload's 32 experts, or 256 with
+        # sigmoid scores and a selection bias
+        wide = args.profile == "router_wide"
+        g = torch.Generator(device="cuda").manual_seed(0)
+        E, K = (256, 8) if wide else (32, 8)
+        logits = torch.randn((16384, E), generator=g, device="cuda") * 1.2
+        logits = logits if wide else logits.to(torch.bfloat16)
+        opt = {"sigmoid": wide, "loss_coef": 0.01}
+        bias = torch.randn(E, generator=g, device="cuda") * 0.1 if wide else None
+
+        def router_step():
+            idx, w, counts, _, loss = sat.router_topk(logits, K, bias=bias, **opt)
+            sat.router_topk_bwd(logits, idx, w, counts=counts, grad_loss=loss, **opt)
+        calls = {args.profile: router_step}
+    elif args.profile in ("swiglu_stash", "swiglu_bwd", "swiglu_bwd_quant"):
+        d = synthetic.swiglu()
+        g, u = synthetic.to_torch_bf16(d["gate"]).cuda(), synthetic.to_torch_bf16(d["up"]).cuda()
+        w = torch.linspace(0.0, 1.0, g.shape[0], device="cuda")
+        stash = sat.swiglu_quant_stash(g, u, row_weights=w)[2:]
+        calls = {"swiglu_stash": lambda: sat.swiglu_quant_stash(g, u, row_weights=w),
+                 "swiglu_bwd": lambda: sat.swiglu_bwd(*stash, u, row_weights=w),
+                 "swiglu_bwd_quant": lambda: sat.swiglu_bwd_quant(*stash, u, row_weights=w)}
+    elif args.profile in ("mxfp4_quantize", "mxfp4_matmul", "mxfp4_token"):
+        x = synthetic.to_torch_bf16(synthetic.dense(seed=0)["x"]).cuda()
+        a, b = sat.quantize_rowwise_mxfp4(x), sat.quantize_rowwise_mxfp4(x[:4096].contiguous())
+        one = sat.quantize_rowwise_mxfp4(x[:1].contiguous())
+        calls = {"mxfp4_quantize": lambda: sat.quantize_rowwise_mxfp4(x),
+                 "mxfp4_matmul": lambda: sat.matmul_mxfp4(*a, *b),
+                 "mxfp4_token": lambda: sat.matmul_mxfp4(*one, *b)}
+    elif args.profile in ("mxfp4_permute", "mxfp4_experts"):
+        d = synthetic.moe(tokens=4096)
+        x = synthetic.to_torch_bf16(d["x"]).cuda()
+        idx, E = torch.from_numpy(d["topk_idx"]).cuda(), d["num_experts"]
+        q, sf, off, _ = sat.permute_pad_mxfp4(x, idx, E, 128)
+        w = sat.quantize_rowwise_mxfp4(torch.randn((E * 2048, x.shape[1]), device="cuda").to(torch.bfloat16))
+        out = torch.zeros((q.shape[0], 2048), dtype=torch.bfloat16, device="cuda")
+        calls = {"mxfp4_permute": lambda: sat.permute_pad_mxfp4(x, idx, E, 128),
+                 "mxfp4_experts": lambda: sat.matmul_mxfp4(q, sf, *w, group_offsets=off, out=out)}
     else:  # permute
         d = synthetic.moe()
         x = synthetic.to_torch_bf16(d["x"]).cuda()
@@ -884,7 +932,9 @@ def main(argv=None):
     ap.add_argument("--profile", choices=["quantize", "direct", "naive", "swiglu", "permute", "rowwise_colwise",
                                           "unpermute", "unpermute_fp8", "mx32", "permute_fp8", "mx32_quantize",
                                           "direct_grouped", "ep_pack", "ep_recv", "direct_stress", "permute_e512",
-                                          "permute_e4096", "unpermute_fp8_k"],
+                                          "permute_e4096", "unpermute_fp8_k", "router", "router_wide",
+                                          "swiglu_stash", "swiglu_bwd", "swiglu_bwd_quant", "mxfp4_quantize",
+                                          "mxfp4_permute", "mxfp4_matmul", "mxfp4_token", "mxfp4_experts"],
                     default=None,
                     help="launch only this kernel (for ncu captures); prints no bench line")
     args = ap.parse_args(argv)

@@ -436,7 +436,7 @@ fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id
  *   drow_weights[row] = sum over the row of dy*g*s*u      (out, fp32 [rows], or NULL; only
  *                       with row_weights), summed in a fixed order.
  * fp8q_swiglu_bwd_quant: the same gradients as row-wise E4M3 pairs (dgq, dgsf), (duq, dusf)
- * by the rule of fp8q_quantize_rowwise applied to the fp32 values, ready for the FP8 products and
+ * by the rule of fp8q_quantize_rowwise on their fp32 values, ready for the FP8 products and
  * fp8q_direct_transpose (dense or grouped); with yq, ysf (both or neither) also y = g*s*u*w
  * recomputed from the codes, so that the forward's q need not be kept.
  *
@@ -490,7 +490,8 @@ fp8q_status fp8q_swiglu_bwd_quant(const uint8_t *gq, const uint8_t *gsf, const u
  *       A's times group g's B.  Rows of out past the last group are not written; a group
  *       may be empty.  Violations found on the device set FP8Q_ERR_SHAPE in the status word
  *       and skip the offending tiles.
- *   n is any size in the dense form.  m == 0 or n == 0 is a no-op; k == 0 is FP8Q_ERR_SHAPE.
+ *   n is any size in the dense form; k at most 2^24.  m == 0 or n == 0 is a no-op; k == 0 is
+ *   FP8Q_ERR_SHAPE.
  *   A scale byte 255 (NaN) makes its products NaN.  Alignment 16 bytes (group_offsets 4).
  *   Errors: NULL, ALIGN, SHAPE, ARG (num_groups), CUDA; TIMEOUT in the status word. */
 size_t fp8q_mxfp4_sf_bytes(int64_t rows, int64_t k);

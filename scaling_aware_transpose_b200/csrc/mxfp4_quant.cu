@@ -36,6 +36,12 @@ __device__ __forceinline__ Unit quantize_unit(const uint4& a, const uint4& b, in
   return u;
 }
 
+// Row of unit u and its position in the row; 32-bit where every unit fits.
+__device__ __forceinline__ void split_unit(int64_t u, int k128, bool small, int64_t& row, int64_t& c4) {
+  row = small ? (int64_t)((uint32_t)u / (uint32_t)k128) : u / k128;
+  c4 = u - row * k128;
+}
+
 // Rows up to the next multiple of 128 get scale bytes (127) and no codes.
 __global__ void __launch_bounds__(kThreads) quantize_mxfp4_kernel(const uint4* __restrict__ x, int64_t rows,
                                                                   int k128, int64_t n_units, uint2* __restrict__ q,
@@ -62,8 +68,9 @@ __global__ void __launch_bounds__(kThreads) quantize_mxfp4_kernel(const uint4* _
     const Unit v = quantize_unit(a[i], b[i], sub);
     if (u < live) q[u * 8 + sub] = v.codes;
     if (u < n_units && sub == 0) {
-      const int64_t r = u / k128;
-      *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, u - r * k128, k128)) = v.scales;
+      int64_t r, c4;
+      split_unit(u, k128, (n_units >> 32) == 0, r, c4);
+      *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, c4, k128)) = v.scales;
     }
   }
 }
@@ -111,13 +118,24 @@ __global__ void __launch_bounds__(kThreads) scatter_mxfp4_kernel(const uint4* __
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int64_t u = first + 4 * i;
-    if (u >= n_units) continue;
-    const int64_t t = u / k128, c4 = u - t * k128;
-    for (int k = 0; k < topk; ++k) {
-      const int64_t r = ld_g(row_id_map + t * topk + k);
-      if (r < 0 || r >= max_rows) continue;  // (never out of range for a consistent routing)
-      q[(r * k128 + c4) * 8 + sub] = v[i].codes;
-      if (sub == 0) *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, c4, k128)) = v[i].scales;
+    int64_t t, c4;
+    split_unit(u, k128, (n_units >> 32) == 0, t, c4);
+    // Eight destinations at a time: lane `sub` reads one's row, stores its scales and hands the
+    // row to the other lanes, which all store codes.
+    for (int k0 = 0; k0 < topk; k0 += 8) {
+      int32_t mine = -1;
+      if (u < n_units && k0 + sub < topk) {
+        const int32_t r = ld_g(row_id_map + t * topk + k0 + sub);
+        if (r >= 0 && r < max_rows) {  // (never out of range for a consistent routing)
+          mine = r;
+          *reinterpret_cast<uint32_t*>(sf + sf_word_offset(r, c4, k128)) = v[i].scales;
+        }
+      }
+      const int n = min(8, topk - k0);
+      for (int k = 0; k < n; ++k) {
+        const int32_t r = __shfl_sync(0xFFFFFFFFu, mine, k, 8);
+        if (r >= 0) q[((int64_t)r * k128 + c4) * 8 + sub] = v[i].codes;
+      }
     }
   }
 }

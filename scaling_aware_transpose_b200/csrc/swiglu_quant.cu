@@ -427,7 +427,8 @@ __global__ void __launch_bounds__(kStashThreads, kStashCtas) swiglu_stash_kernel
       mul2_rn(y[2 * k], y[2 * k + 1], lo, hi);
     }
     if (row_weights != nullptr) {
-      const float w = live ? ld_g(row_weights + (uint64_t)tile / tiles_per_row) : 0.0f;
+      const uint64_t row = n_tiles >> 32 ? (uint64_t)tile / tiles_per_row : (uint32_t)tile / tiles_per_row;
+      const float w = live ? ld_g(row_weights + row) : 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) mul2_rn(y[2 * k], y[2 * k + 1], w, w);
     }

@@ -162,7 +162,7 @@ def test_mxfp4_matmul_refusals(L):
     def f(aq=A, asf=A, m=4, bq=A, bsf=A, n=128, k=256, off=None, G=1, out=A):
         return L.fp8q_matmul_mxfp4(aq, asf, m, bq, bsf, n, k, off, G, out, None)
 
-    for kw in (dict(m=-1), dict(n=-1), dict(k=100), dict(k=0), dict(m=1 << 31), dict(off=A, n=100),
+    for kw in (dict(m=-1), dict(n=-1), dict(k=100), dict(k=0), dict(k=(1 << 24) + 128), dict(m=1 << 31), dict(off=A, n=100),
                dict(off=A, n=1 << 24, G=200)):
         assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
     for kw in (dict(G=0), dict(G=2), dict(off=A, G=0)):
