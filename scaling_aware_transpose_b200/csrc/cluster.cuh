@@ -35,6 +35,11 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_address(addr, rank)) : "memory");
+  return v;
+}
 __device__ __forceinline__ double ld_cluster_f64(uint32_t addr, uint32_t rank) {
   double v;
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(peer_address(addr, rank)) : "memory");

@@ -3,7 +3,9 @@
 //
 // Two lanes per 32-element tile, 16 elements (two 16-byte loads) each: a tile's amax takes
 // one shuffle, and eight lanes hold a 128-element unit whose four scale bytes leave as one
-// word of the tiled layout.  2 B are read and 0.53 B written per element: bound by HBM.
+// word of the tiled layout.  2 B are read and 0.53 B written per element: bound by HBM (8192
+// x 7168: 24.6 us, 6.05 TB/s; 65536 rows: 6.6 TB/s; 4096 x 7168 to 8 of 32 experts: 44 us, of
+// which the routing kernels take 8).
 #include "abi_checks.h"
 #include "launch.h"
 #include "mxfp4.cuh"

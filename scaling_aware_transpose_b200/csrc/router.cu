@@ -19,15 +19,23 @@
 //   softmax: d p_e += g_e;  d l_e = p_e * (d p_e - sum_j d p_j p_j)
 //   sigmoid: d p_e += (g_e - sum_j g_j h_j) / (sum of all p + 1e-20);  d l_e = d p_e * p_e * (1 - p_e)
 //
-// One warp per token, the token's logits in registers (four neighbouring experts a lane and
-// 16-byte loads from 65 experts on), the next token's on their way.  The picks of a row of
-// 65 or more experts come from a short list: the k-th largest of the 32 lanes' maxima bounds
-// the k-th largest value from below, and what reaches it (a dozen, typically) is gathered
-// one to a lane, so that a pick is one warp maximum and a vote instead of a pass over the
-// row.  With a bias the list is made from fp32 scores with a margin for their rounding, and
-// only its members are scored in double.  All sums are fp32 in a fixed order (per lane over
-// the warp's tokens, over the CTA's warps, then over CTAs in double), the counts are
-// integers: nothing depends on the order of atomics.
+// From 129 experts on a warp holds a token: the logits in registers (8 to 32 a lane, 16-byte
+// loads of four neighbours), the next token's on their way.  The picks come from a short
+// list: the k-th largest of the 32 lanes' maxima bounds the k-th largest value from below, and
+// what reaches it (a dozen, typically) is gathered one to a lane, so that a pick is one warp
+// maximum and a vote instead of a pass over the row.  With a bias the list is made from fp32
+// scores with a margin for their rounding, and only its members are scored in double.
+// Up to 128 experts 8 or 16 lanes hold a token and a warp works on four or two.
+// All sums are fp32 in a fixed order (per lane over its tokens, over the warp's tokens, over
+// the CTA's warps, then over CTAs in double), the counts are integers: nothing depends on the
+// order of atomics.
+//
+// What bounds it: the issue of instructions (ncu: 71% of the slots), about 760 a token forward
+// and 450 backward at 256 experts, three quarters of them the warp-wide rounds of the choice
+// and the sums rather than work on the logits.  50021 x 256 fp32 with a bias: 57 us forward
+// with statistics, 33 us backward, against 8 and 16 us for the bytes (passing over the row
+// for every pick: 130 us).  16384 x 32 BF16, four tokens a warp: 11.3 and 4.7 us (a warp a
+// token: 14.5 and 9), of which 5 us are the finishing launch.
 #include <cfloat>
 
 #include "abi_checks.h"
@@ -43,7 +51,6 @@ constexpr int kThreads = 32 * kWarps;
 // CTAs that 148 SMs hold at once: four an SM (64 registers a thread) up to 256 experts, two
 // above.  A fixed number, so that the order of the sums is the same wherever it runs.
 constexpr int resident(int vpl) { return vpl <= 8 ? 4 : 2; }
-constexpr int resident_bwd(int vpl) { return vpl <= 2 ? 5 : resident(vpl); }
 constexpr int max_blocks(int experts) { return 148 * (experts <= 256 ? resident(8) : resident(16)); }
 constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopk = 64;
@@ -68,10 +75,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Expert i of a lane: four neighbours a lane from four experts a lane on.
-template <int VPL>
-__device__ __forceinline__ int expert_of(int lane, int i) {
-  return VPL < 4 ? lane + 32 * i : 4 * lane + 128 * (i >> 2) + (i & 3);
+// Expert i of lane `sub` of the L lanes that hold a token: four neighbours at a time.
+template <int L = 32>
+__device__ __forceinline__ int expert_of(int sub, int i) {
+  return 4 * sub + 4 * L * (i >> 2) + (i & 3);
 }
 
 // NaN counts as -inf (a padding row may hold anything), +inf as the largest finite value.
@@ -112,13 +119,14 @@ __device__ __forceinline__ void sigmoid2(float l, float& p, float& q) {
   q = l >= 0.0f ? s : r;
 }
 
-// A token's logits as they lie in memory (padding lanes: -inf), and cleaned.
-template <int VPL, typename T>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, bool quads, float (&v)[VPL]) {
-  if (VPL >= 4 && quads) {  // E % 4 == 0: whole, aligned quads
+// A token's logits as they lie in memory (padding lanes: -inf).  quads: E % 4 == 0, whole and
+// aligned quads.
+template <int L, int V, typename T>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int sub, bool quads, float (&v)[V]) {
+  if (quads) {
 #pragma unroll
-    for (int j = 0; j < VPL; j += 4) {
-      const int e = expert_of<VPL>(lane, j);
+    for (int j = 0; j < V; j += 4) {
+      const int e = expert_of<L>(sub, j);
       float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (e < E) {
         if constexpr (sizeof(T) == 4) {
@@ -130,43 +138,57 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
         }
       }
       v[j] = f.x;
-      if constexpr (VPL >= 4) {
-        v[j + 1] = f.y;
-        v[j + 2] = f.z;
-        v[j + 3] = f.w;
-      }
+      v[j + 1] = f.y;
+      v[j + 2] = f.z;
+      v[j + 3] = f.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = expert_of<VPL>(lane, i);
+    for (int i = 0; i < V; ++i) {
+      const int e = expert_of<L>(sub, i);
       v[i] = e < E ? to_float<T>(row[e]) : -INFINITY;
     }
   }
 }
-template <int VPL, typename T>
-__device__ __forceinline__ void store_row(T* __restrict__ row, int E, int lane, bool quads, const float (&v)[VPL]) {
-  if (VPL >= 4 && quads) {
+template <int L, int V, typename T>
+__device__ __forceinline__ void store_row(T* __restrict__ row, int E, int sub, bool quads, const float (&v)[V]) {
+  if (quads) {
 #pragma unroll
-    for (int j = 0; j < VPL; j += 4) {
-      const int e = expert_of<VPL>(lane, j);
-      if constexpr (VPL >= 4) {
-        if (e < E) {
-          if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4*>(row + e) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-          else
-            *reinterpret_cast<uint2*>(row + e) = make_uint2(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]));
-        }
+    for (int j = 0; j < V; j += 4) {
+      const int e = expert_of<L>(sub, j);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(row + e) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        else
+          *reinterpret_cast<uint2*>(row + e) = make_uint2(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]));
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = expert_of<VPL>(lane, i);
+    for (int i = 0; i < V; ++i) {
+      const int e = expert_of<L>(sub, i);
       if (e < E) {
         if constexpr (sizeof(T) == 4) row[e] = v[i];
         else row[e] = (T)pack_bf16(v[i], 0.0f);
       }
+    }
+  }
+}
+// A warp's row of gradients in shared memory.
+template <int L, int V>
+__device__ __forceinline__ void read_row(const float* buf, int E, int sub, bool quads, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    if (quads) {
+      const int e = expert_of<L>(sub, j);
+      const float4 f = e < E ? *reinterpret_cast<const float4*>(buf + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      v[j] = f.x;
+      v[j + 1] = f.y;
+      v[j + 2] = f.z;
+      v[j + 3] = f.w;
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 4; ++i) v[i] = expert_of<L>(sub, i) < E ? buf[expert_of<L>(sub, i)] : 0.0f;
     }
   }
 }
@@ -177,6 +199,75 @@ struct RouterArgs {
   bool renorm, stats;
   float scale;
 };
+// Where the balance statistics go: the workspace (then router_finish_kernel sums the CTAs'
+// parts), or with `fused` (one cluster holds every CTA) straight to the results.
+struct StatsOut {
+  uint32_t* ws;
+  int32_t* counts;
+  float* prob_sums;
+  float* loss;
+  float loss_coef;
+  bool fused;
+};
+
+__device__ __forceinline__ float loss_of(const RouterArgs& a, float loss_coef, double dot, long long c) {
+  return c > 0 ? (float)((double)loss_coef * a.E * a.topk / ((double)c * (double)c) * dot) : 0.0f;
+}
+
+// The CTA's sums and counts (complete, behind a barrier).  Workspace: [0] a counter for the
+// finishing kernel, then per CTA E sums (fp32), then per CTA E counts (int32), from byte 16 on.
+__device__ __forceinline__ void publish(const float* sums, const int* counts, const RouterArgs& a, const StatsOut& out) {
+  if (!out.fused) {
+    float* part = reinterpret_cast<float*>(out.ws + 4);
+    int32_t* part_n = reinterpret_cast<int32_t*>(part + (int64_t)gridDim.x * a.E);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      part[(int64_t)blockIdx.x * a.E + e] = sums[e];
+      part_n[(int64_t)blockIdx.x * a.E + e] = counts[e];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) out.ws[0] = 0u;
+    return;
+  }
+  __shared__ double dot_sh[kWarps];
+  __shared__ long long c_sh[kWarps];
+  const uint32_t size = cluster_size();
+  __syncthreads();
+  cluster_sync();
+  if (cluster_rank() == 0) {
+    double dot = 0.0;
+    long long c = 0;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      double s = 0.0;
+      int n = 0;
+      for (uint32_t r = 0; r < size; ++r) {  // in rank order
+        s += (double)ld_cluster_f32(smem_u32(sums + e), r);
+        n += ld_cluster_s32(smem_u32(counts + e), r);
+      }
+      out.counts[e] = n;
+      out.prob_sums[e] = (float)s;
+      dot += (double)n * (double)(float)s;
+      c += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      dot += __shfl_xor_sync(kAll, dot, o);
+      c += __shfl_xor_sync(kAll, c, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+      dot_sh[threadIdx.x >> 5] = dot;
+      c_sh[threadIdx.x >> 5] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWarps; ++w) {
+        dot += dot_sh[w];
+        c += c_sh[w];
+      }
+      *out.loss = loss_of(a, out.loss_coef, dot, c);
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // the first CTA has read the others' sums
+}
 
 // ------------------------------------------------------------------ selection
 struct Pick {
@@ -196,13 +287,12 @@ __device__ __forceinline__ void bias_keys(float l, float bias, uint32_t& hi, uin
 
 // Any row: each pick passes over the whole row.  Writes the k picks, best first.
 template <int VPL, int MODE, typename T>
-__device__ __forceinline__ void pick_all(const T* __restrict__ row, const float* __restrict__ bias, int E, int K,
-                                         int lane, Pick* __restrict__ picks) {
+__device__ __noinline__ void pick_all(const T* row, const float* bias, int E, int K, int lane, Pick* picks) {
   uint32_t key[VPL];
   uint32_t key_lo[MODE == kSigmoidBias ? VPL : 1];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = expert_of<VPL>(lane, i);
+    const int e = expert_of(lane, i);
     key[i] = 0u;
     if (MODE == kSigmoidBias) key_lo[i] = 0u;
     if (e < E) {
@@ -225,17 +315,13 @@ __device__ __forceinline__ void pick_all(const T* __restrict__ row, const float*
       m_lo = __reduce_max_sync(kAll, b);
     }
     uint32_t e = 0xFFFFu;
-    if (VPL == 1) {  // the lowest lane is the lowest id
-      e = __ffs(__ballot_sync(kAll, key[0] == m && (MODE != kSigmoidBias || key_lo[0] == m_lo))) - 1;
-    } else {
 #pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = expert_of<VPL>(lane, i);
-      e = __reduce_min_sync(kAll, e);
-    }
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == m && (MODE != kSigmoidBias || key_lo[i] == m_lo)) e = expert_of(lane, i);
+    e = __reduce_min_sync(kAll, e);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (e == (uint32_t)expert_of<VPL>(lane, i)) key[i] = 0u;
+      if (e == (uint32_t)expert_of(lane, i)) key[i] = 0u;
     if (lane == 0) {
       picks[s].e = (int)e;
       picks[s].l = MODE == kSigmoidBias ? clean(to_float<T>(row[e])) : from_key(m);
@@ -243,11 +329,6 @@ __device__ __forceinline__ void pick_all(const T* __restrict__ row, const float*
   }
   __syncwarp();
 }
-template <int VPL, int MODE, typename T>
-__device__ __noinline__ void pick_all_call(const T* row, const float* bias, int E, int K, int lane, Pick* picks) {
-  pick_all<VPL, MODE, T>(row, bias, E, K, lane, picks);
-}
-
 // How far an fp32 score sigmoid2(l) + bias may be from the exact one: the sigmoid by 2^-21
 // (1.5 |l| + 4 half steps of the exponential times s (1 - s), and 4 more, are 5.4 half steps),
 // the sum by half a step; the rest covers the arithmetic on the bound itself.
@@ -278,7 +359,7 @@ __device__ __forceinline__ bool pick_listed(const float (&order)[VPL], const flo
     const int at = n + __popc(mask & ((1u << lane) - 1u));
     if (in && at < 32) {
       picks[at].l = val[i];
-      picks[at].e = expert_of<VPL>(lane, i);
+      picks[at].e = expert_of(lane, i);
     }
     n += __popc(mask);
   }
@@ -317,13 +398,11 @@ __device__ __forceinline__ bool pick_listed(const float (&order)[VPL], const flo
 }
 
 // ------------------------------------------------------------------ forward
-// Workspace: [0] a counter for the finishing kernel, then per CTA E sums (fp32), then per
-// CTA E counts (int32), from byte 16 on.
 template <int VPL, int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T* __restrict__ logits, const float* __restrict__ bias,
                                                           const uint8_t* __restrict__ mask, RouterArgs a,
                                                           int32_t* __restrict__ topk_idx, float* __restrict__ weights,
-                                                          uint32_t* __restrict__ ws) {
+                                                          StatsOut out) {
   constexpr int kSlots = 32 * VPL;
   __shared__ float sums_sh[kSlots];
   __shared__ int counts_sh[kSlots];
@@ -348,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
   const int64_t stride = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + wid;
   float next[VPL];
-  if (kAhead && t < a.tokens) load_row<VPL, T>(logits + t * E, E, lane, quads, next);
+  if (kAhead && t < a.tokens) load_row<32, VPL, T>(logits + t * E, E, lane, quads, next);
   for (; t < a.tokens; t += stride) {
     const T* row = logits + t * E;
     const bool live = mask == nullptr || mask[t] != 0;
@@ -356,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
     if (kAhead) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) val[i] = clean(next[i]);
-      if (t + stride < a.tokens) load_row<VPL, T>(row + stride * E, E, lane, quads, next);
+      if (t + stride < a.tokens) load_row<32, VPL, T>(row + stride * E, E, lane, quads, next);
     } else {
-      load_row<VPL, T>(row, E, lane, quads, val);
+      load_row<32, VPL, T>(row, E, lane, quads, val);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) val[i] = clean(val[i]);
     }
@@ -369,23 +448,19 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
       for (int i = 0; i < VPL; ++i) sigmoid2(val[i], p[i], q);
     }
     // ---- the k picks
-    if constexpr (VPL < 4) {
-      pick_all<VPL, MODE, T>(row, bias, E, K, lane, picks);
-    } else {
-      bool done = false;
-      if (K <= kListTopk) {
-        if (MODE == kSigmoidBias) {
-          float order[VPL];
-          load_row<VPL, float>(bias, E, lane, quads && bias_quads, order);  // (padding lanes: -inf)
+    bool done = false;
+    if (K <= kListTopk) {
+      if (MODE == kSigmoidBias) {
+        float order[VPL];
+        load_row<32, VPL, float>(bias, E, lane, quads && bias_quads, order);  // (padding lanes: -inf)
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) order[i] += p[i];
-          done = pick_listed<VPL, MODE>(order, val, bias, K, lane, picks);
-        } else {
-          done = pick_listed<VPL, MODE>(val, val, bias, K, lane, picks);
-        }
+        for (int i = 0; i < VPL; ++i) order[i] += p[i];
+        done = pick_listed<VPL, MODE>(order, val, bias, K, lane, picks);
+      } else {
+        done = pick_listed<VPL, MODE>(val, val, bias, K, lane, picks);
       }
-      if (!done) pick_all_call<VPL, MODE, T>(row, bias, E, K, lane, picks);
     }
+    if (!done) pick_all<VPL, MODE, T>(row, bias, E, K, lane, picks);
     Pick mine[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) mine[h] = lane + 32 * h < K ? picks[lane + 32 * h] : Pick{-INFINITY, 0};
@@ -450,32 +525,238 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
     if (wid == w) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (expert_of<VPL>(lane, i) < E) sums_sh[expert_of<VPL>(lane, i)] += acc[i];
+        if (expert_of(lane, i) < E) sums_sh[expert_of(lane, i)] += acc[i];
     }
     __syncthreads();
   }
-  float* part = reinterpret_cast<float*>(ws + 4);
-  int32_t* part_n = reinterpret_cast<int32_t*>(part + (int64_t)gridDim.x * E);
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    part[(int64_t)blockIdx.x * E + e] = sums_sh[e];
-    part_n[(int64_t)blockIdx.x * E + e] = counts_sh[e];
+  publish(sums_sh, counts_sh, a, out);
+}
+
+// ------------------------------------------------------------------ up to 128 experts
+// L lanes (8 or 16) hold a token, 4 or 8 experts a lane, and a warp works on 32 / L tokens at
+// once: the rounds of the choice and the sums, which are most of the work, serve them
+// together.  Maxima and sums go by shuffles within the L lanes; every lane of the warp takes
+// every step, a group past the last token on -inf.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1) v = min(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+template <int L, int V, int MODE, typename T>
+__global__ void __launch_bounds__(kThreads, 4) router_small_kernel(const T* __restrict__ logits,
+                                                                   const float* __restrict__ bias,
+                                                                   const uint8_t* __restrict__ mask, RouterArgs a,
+                                                                   int32_t* __restrict__ topk_idx,
+                                                                   float* __restrict__ weights, StatsOut out) {
+  constexpr int kGroups = 32 / L;
+  __shared__ float sums_sh[L * V];
+  __shared__ int counts_sh[L * V];
+  __shared__ Pick picks_sh[kWarps][kGroups][kRouterMaxTopk];
+  pdl_wait_for(logits, bias, mask);
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, sub = lane & (L - 1), grp = lane / L;
+  const int E = a.E, K = a.topk;
+  const bool quads = (E & 3) == 0;
+  Pick* picks = picks_sh[wid][grp];
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  if (a.stats) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      sums_sh[e] = 0.0f;
+      counts_sh[e] = 0;
+    }
+    __syncthreads();
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) ws[0] = 0u;
+  const int64_t stride = (int64_t)gridDim.x * kWarps * kGroups;
+  int64_t t = ((int64_t)blockIdx.x * kWarps + wid) * kGroups + grp;
+  float next[V];
+  auto load = [&](int64_t u) {
+    if (u < a.tokens) {
+      load_row<L, V, T>(logits + u * E, E, sub, quads, next);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+    }
+  };
+  load(t);
+  for (; t - grp < a.tokens; t += stride) {  // the warp's first token decides for all
+    const bool here = t < a.tokens;
+    const bool live = here && (mask == nullptr || mask[t] != 0);
+    const T* row = logits + (here ? t : 0) * E;
+    float val[V];
+    uint32_t key[V], key_lo[MODE == kSigmoidBias ? V : 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) val[i] = clean(next[i]);
+    load(t + stride);
+    // ---- the k picks, by `key` (and under a bias its remainder `key_lo`).  With `check`, one
+    // round more: true if two neighbours in the order may be closer than their fp32 errors.
+    auto choose = [&](bool check) {
+      bool close = false;
+      float before = INFINITY;
+      for (int s = 0; s < K + (check ? 1 : 0); ++s) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) best = max(best, key[i]);
+        const uint32_t m = group_max<L>(best);
+        if (check) {
+          const float f = from_key(m);
+          close |= s > 0 && s < E && !(before - f > 2.0f * score_error(before));
+          before = f;
+          if (s == K) break;
+        }
+        uint32_t m_lo = 0u;
+        if (MODE == kSigmoidBias && !check) {
+          uint32_t b = 0u;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (key[i] == m) b = max(b, key_lo[i]);
+          m_lo = group_max<L>(b);
+        }
+        uint32_t e = 0xFFFFu;
+        float l = 0.0f;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == m && (MODE != kSigmoidBias || check || key_lo[i] == m_lo)) {
+            e = expert_of<L>(sub, i);
+            l = val[i];
+          }
+        const uint32_t first = group_min<L>(e);
+        if (e == first) {  // the lane that holds it
+          picks[s].e = (int)e;
+          picks[s].l = l;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (first == (uint32_t)expert_of<L>(sub, i)) key[i] = 0u;
+      }
+      __syncwarp();
+      return close;
+    };
+    if (MODE == kSigmoidBias) {
+      // fp32 scores decide where they can; where some token's are too close, the warp's tokens
+      // are scored in double (for every token that cost half of the kernel's time).
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = expert_of<L>(sub, i);
+        float p, q;
+        sigmoid2(val[i], p, q);
+        const float score = e < E ? p + bias[e] : 0.0f;
+        key[i] = e < E ? order_key(score == score ? score : -INFINITY) : 0u;
+      }
+      if (__any_sync(kAll, choose(true) && here)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = expert_of<L>(sub, i);
+          key[i] = key_lo[i] = 0u;
+          if (e < E) bias_keys(val[i], bias[e], key[i], key_lo[i]);
+        }
+        choose(false);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = expert_of<L>(sub, i) < E ? order_key(val[i]) : 0u;
+      choose(false);
+    }
+    const float top = picks[0].l;  // (softmax: the row's maximum)
+    // ---- probabilities
+    float z_inv = 1.0f;
+    if (MODE == kSoftmax) {
+      if (a.stats || !a.renorm) {
+        float p[V], z = 0.0f;
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[i] = exp_neg(val[i] - base);
+          z += p[i];
+        }
+        z = group_sum<L>(z);
+        z_inv = z > 0.0f ? rcp(z) : 0.0f;
+        const float share = live ? z_inv : 0.0f;
+        if (a.stats) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(p[i], share, acc[i]);
+        }
+      }
+    } else if (a.stats) {
+      float p[V], q, z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sigmoid2(val[i], p[i], q);
+        z += p[i];
+      }
+      z = group_sum<L>(z);
+      const float share = live ? rcp(z + kEps) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(p[i], share, acc[i]);
+    }
+    auto weight = [&](float l) {
+      float w, q;
+      if (MODE == kSoftmax) {
+        w = top == -INFINITY ? 0.0f : exp_neg(l - top);
+        return a.renorm ? w : w * z_inv;
+      }
+      sigmoid2(l, w, q);
+      return w;
+    };
+    float total = 0.0f;
+    if (a.renorm)
+      for (int s = sub; s < K; s += L) total += weight(picks[s].l);
+    const float factor = a.renorm ? a.scale * rcp(group_sum<L>(total) + kEps) : a.scale;
+    if (here) {
+      for (int s = sub; s < K; s += L) {
+        const Pick p = picks[s];
+        topk_idx[t * K + s] = p.e;
+        weights[t * K + s] = live ? weight(p.l) * factor : 0.0f;
+        if (a.stats && live) atomicAdd(&counts_sh[p.e], 1);
+      }
+    }
+    __syncwarp();
+  }
+  if (!a.stats) return;
+#pragma unroll
+  for (int o = L; o < 32; o <<= 1)  // over the warp's tokens
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = __fadd_rn(acc[i], __shfl_xor_sync(kAll, acc[i], o));
+  for (int w = 0; w < kWarps; ++w) {  // the warps' sums in order
+    if (wid == w && grp == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (expert_of<L>(sub, i) < E) sums_sh[expert_of<L>(sub, i)] += acc[i];
+    }
+    __syncthreads();
+  }
+  publish(sums_sh, counts_sh, a, out);
 }
 
 // Sums the CTAs' partial results: a cluster of CTAs per 32 experts, its warps sharing the
 // rows (10 each at most, all on their way at once), the CTAs' sums joined in rank order; the
 // last cluster to finish (the counter was zeroed by the kernel before) forms the loss.
 constexpr int kFinishCluster = 8;
-__global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int E, int topk, float loss_coef,
-                                                                 uint32_t* __restrict__ ws, int32_t* __restrict__ counts,
-                                                                 float* __restrict__ prob_sums,
-                                                                 float* __restrict__ loss) {
+__global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, RouterArgs a, StatsOut out) {
   __shared__ double sum_sh[kWarps][32];
   __shared__ int cnt_sh[kWarps][32];
   __shared__ bool last;
-  pdl_wait_for(ws, counts, prob_sums);
+  pdl_wait_for(out.ws, out.counts, out.prob_sums);
   pdl_trigger();
+  const int E = a.E;
+  uint32_t* ws = out.ws;
+  int32_t* counts = out.counts;
+  float* prob_sums = out.prob_sums;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int e = blockIdx.x / size * 32 + lane;
@@ -550,12 +831,29 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, int
     dot += __shfl_xor_sync(kAll, dot, o);
     c += __shfl_xor_sync(kAll, c, o);
   }
-  if (lane == 0) *loss = c > 0 ? (float)((double)loss_coef * E * topk / ((double)c * (double)c) * dot) : 0.0f;
+  if (lane == 0) *out.loss = loss_of(a, out.loss_coef, dot, c);
 }
 
 // ------------------------------------------------------------------ backward
+// g_e of every expert into shared memory; ends with a barrier.
+__device__ __forceinline__ void balance_slopes(const int32_t* counts, const RouterArgs& a, float loss_coef,
+                                               const float* grad_loss, float* g_sh) {
+  __shared__ long long c_sh[kWarps];
+  long long c = 0;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) c += counts[e];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) c += __shfl_xor_sync(kAll, c, o);
+  if ((threadIdx.x & 31) == 0) c_sh[threadIdx.x >> 5] = c;
+  __syncthreads();
+  c = 0;
+  for (int w = 0; w < kWarps; ++w) c += c_sh[w];
+  const double f = c > 0 ? (double)*grad_loss * (double)loss_coef * a.E * a.topk / ((double)c * (double)c) : 0.0;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) g_sh[e] = (float)(f * (double)counts[e]);
+  __syncthreads();
+}
+
 template <int VPL, bool SIGMOID, typename T>
-__global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel(const T* __restrict__ logits,
+__global__ void __launch_bounds__(kThreads, resident(VPL)) router_bwd_kernel(const T* __restrict__ logits,
                                                               const uint8_t* __restrict__ mask, RouterArgs a,
                                                               const int32_t* __restrict__ topk_idx,
                                                               const float* __restrict__ grad_weights,
@@ -564,7 +862,6 @@ __global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel
                                                               const float* __restrict__ grad_loss,
                                                               T* __restrict__ grad, int* status) {
   extern __shared__ __align__(16) float sh[];  // g_e, then a row per warp
-  __shared__ long long c_sh[kWarps];
   pdl_wait_for(logits, mask, topk_idx, grad_weights, row_id_map, counts, grad_loss);
   pdl_trigger();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -573,34 +870,22 @@ __global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel
   float* g_sh = sh;
   const int pitch = (E + 3) & ~3;  // rows on 16 bytes
   float* buf = sh + (1 + wid) * pitch;
-  if (balance) {
-    long long c = 0;
-    for (int e = threadIdx.x; e < E; e += kThreads) c += counts[e];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) c += __shfl_xor_sync(kAll, c, o);
-    if (lane == 0) c_sh[wid] = c;
-    __syncthreads();
-    c = 0;
-    for (int w = 0; w < kWarps; ++w) c += c_sh[w];
-    const double f = c > 0 ? (double)*grad_loss * (double)loss_coef * E * K / ((double)c * (double)c) : 0.0;
-    for (int e = threadIdx.x; e < E; e += kThreads) g_sh[e] = (float)(f * (double)counts[e]);
-    __syncthreads();
-  }
+  if (balance) balance_slopes(counts, a, loss_coef, grad_loss, g_sh);
   float g[VPL];  // this lane's g_e
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) g[i] = balance && expert_of<VPL>(lane, i) < E ? g_sh[expert_of<VPL>(lane, i)] : 0.0f;
+  for (int i = 0; i < VPL; ++i) g[i] = balance && expert_of(lane, i) < E ? g_sh[expert_of(lane, i)] : 0.0f;
   const bool quads = (E & 3) == 0;
   // A row of zeros per warp, into which the chosen experts' gradients are put and taken out
   // again.
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (expert_of<VPL>(lane, i) < E) buf[expert_of<VPL>(lane, i)] = 0.0f;
+    if (expert_of(lane, i) < E) buf[expert_of(lane, i)] = 0.0f;
   __syncwarp();
   constexpr bool kAhead = VPL <= 8;
   const int64_t stride = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + wid;
   float next[VPL];
-  if (kAhead && t < a.tokens) load_row<VPL, T>(logits + t * E, E, lane, quads, next);
+  if (kAhead && t < a.tokens) load_row<32, VPL, T>(logits + t * E, E, lane, quads, next);
   int next_id[2] = {-1, -1};  // this lane's slots of the next token: expert (or -1), gradient
   float next_dw[2] = {0.0f, 0.0f};
   auto load_slots = [&](int64_t u) {
@@ -629,16 +914,16 @@ __global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel
     if (kAhead) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) p[i] = clean(next[i]);
-      if (t + stride < a.tokens) load_row<VPL, T>(row + stride * E, E, lane, quads, next);
+      if (t + stride < a.tokens) load_row<32, VPL, T>(row + stride * E, E, lane, quads, next);
     } else {
-      load_row<VPL, T>(row, E, lane, quads, p);
+      load_row<32, VPL, T>(row, E, lane, quads, p);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) p[i] = clean(p[i]);
     }
     if (mask != nullptr && mask[t] == 0) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) p[i] = 0.0f;
-      store_row<VPL, T>(grad + t * E, E, lane, quads, p);
+      store_row<32, VPL, T>(grad + t * E, E, lane, quads, p);
       if (t + stride < a.tokens) load_slots(t + stride);
       continue;
     }
@@ -728,24 +1013,7 @@ __global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
     if (grad_weights != nullptr) {
-      if (VPL >= 4 && quads) {
-#pragma unroll
-        for (int j = 0; j < VPL; j += 4) {
-          if constexpr (VPL >= 4) {
-            if (expert_of<VPL>(lane, j) < E) {
-              const float4 f = *reinterpret_cast<const float4*>(buf + expert_of<VPL>(lane, j));
-              d[j] = f.x;
-              d[j + 1] = f.y;
-              d[j + 2] = f.z;
-              d[j + 3] = f.w;
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (expert_of<VPL>(lane, i) < E) d[i] = buf[expert_of<VPL>(lane, i)];
-      }
+      read_row<32, VPL>(buf, E, lane, quads, d);
       __syncwarp();
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -766,7 +1034,165 @@ __global__ void __launch_bounds__(kThreads, resident_bwd(VPL)) router_bwd_kernel
 #pragma unroll
       for (int i = 0; i < VPL; ++i) d[i] = (p[i] * unit) * ((balance ? d[i] + g[i] : d[i]) - all);
     }
-    store_row<VPL, T>(grad + t * E, E, lane, quads, d);
+    store_row<32, VPL, T>(grad + t * E, E, lane, quads, d);
+    __syncwarp();
+  }
+}
+
+// Up to 128 experts: L lanes a token, as in router_small_kernel.
+template <int L, int V, bool SIGMOID, typename T>
+__global__ void __launch_bounds__(kThreads, 4) router_small_bwd_kernel(
+    const T* __restrict__ logits, const uint8_t* __restrict__ mask, RouterArgs a, const int32_t* __restrict__ topk_idx,
+    const float* __restrict__ grad_weights, const int32_t* __restrict__ row_id_map, int64_t rows,
+    const int32_t* __restrict__ counts, float loss_coef, const float* __restrict__ grad_loss, T* __restrict__ grad,
+    int* status) {
+  constexpr int kGroups = 32 / L;
+  __shared__ float g_sh[L * V];
+  __shared__ __align__(16) float buf_sh[kWarps][kGroups][L * V];
+  pdl_wait_for(logits, mask, topk_idx, grad_weights, row_id_map, counts, grad_loss);
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, sub = lane & (L - 1), grp = lane / L;
+  const int E = a.E, K = a.topk;
+  const bool balance = grad_loss != nullptr, quads = (E & 3) == 0;
+  float* buf = buf_sh[wid][grp];
+  if (balance) balance_slopes(counts, a, loss_coef, grad_loss, g_sh);
+  float g[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = expert_of<L>(sub, i);
+    g[i] = balance && e < E ? g_sh[e] : 0.0f;
+    buf[e] = 0.0f;
+  }
+  __syncwarp();
+  const int64_t stride = (int64_t)gridDim.x * kWarps * kGroups;
+  for (int64_t t = ((int64_t)blockIdx.x * kWarps + wid) * kGroups + grp; t - grp < a.tokens; t += stride) {
+    const bool here = t < a.tokens;
+    const bool live = here && (mask == nullptr || mask[t] != 0);
+    const T* row = logits + (here ? t : 0) * E;
+    float p[V], q[SIGMOID ? V : 1], unused;
+    if (live) {
+      load_row<L, V, T>(row, E, sub, quads, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = -INFINITY;
+    }
+    float base = 0.0f;
+    if (SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sigmoid2(clean(p[i]), p[i], q[i]);
+    } else {
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        p[i] = clean(p[i]);
+        m = fmaxf(m, p[i]);
+      }
+#pragma unroll
+      for (int o = L / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+      base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = exp_neg(p[i] - base);
+    }
+    // Slot s of a live token: its expert (-1: to be skipped) and its weight's gradient.
+    auto slot = [&](int s, float& dw) {
+      const int e = topk_idx[t * K + s];
+      int64_t at = t * K + s;
+      bool ok = e >= 0 && e < E;
+      if (row_id_map != nullptr) {
+        at = row_id_map[at];
+        ok = ok && at >= 0 && at < rows;
+      }
+      dw = ok ? grad_weights[at] : 0.0f;
+      return ok ? e : -1;
+    };
+    const bool slots = live && grad_weights != nullptr;
+    float z = 0.0f, gp = 0.0f, total = 0.0f, dot = 0.0f, dw;
+    if (slots) {
+      for (int s = sub; s < K; s += L) {
+        const int e = slot(s, dw);
+        if (e < 0) {
+          record_status(status, FP8Q_ERR_DEVICE);
+          continue;
+        }
+        float ps = clean(to_float<T>(row[e]));
+        if (SIGMOID) sigmoid2(ps, ps, unused);
+        else ps = exp_neg(ps - base);
+        total += ps;
+        dot = __fmaf_rn(dw, ps, dot);
+        buf[e] = __int_as_float(1 + s);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      z += p[i];
+      gp = __fmaf_rn(g[i], p[i], gp);
+    }
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) {
+      z = __fadd_rn(z, __shfl_xor_sync(kAll, z, o));
+      gp = __fadd_rn(gp, __shfl_xor_sync(kAll, gp, o));
+      total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+      dot = __fadd_rn(dot, __shfl_xor_sync(kAll, dot, o));
+    }
+    const float z_inv = SIGMOID ? rcp(z + kEps) : (z > 0.0f ? rcp(z) : 0.0f);
+    const float unit = SIGMOID ? 1.0f : z_inv;  // as in router_bwd_kernel
+    const float inv = a.renorm ? rcp(total * unit + kEps) : 1.0f;
+    const float mean = a.renorm ? dot * unit * inv : 0.0f;
+    const float own = a.scale * inv;
+    bool repeated = false;
+    __syncwarp();
+    if (slots)
+      for (int s = sub; s < K; s += L) {
+        const int e = slot(s, dw);
+        repeated |= e >= 0 && __float_as_int(buf[e]) != 1 + s;
+      }
+    __syncwarp();
+    if (!__any_sync(kAll, repeated)) {
+      if (slots)
+        for (int s = sub; s < K; s += L) {
+          const int e = slot(s, dw);
+          if (e >= 0) buf[e] = own * (dw - mean);
+        }
+    } else {  // ids that a caller repeated: one slot after the other
+      if (slots)
+        for (int s = sub; s < K; s += L) {
+          const int e = slot(s, dw);
+          if (e >= 0) buf[e] = 0.0f;
+        }
+      __syncwarp();
+      for (int s = 0; s < K; ++s) {
+        if (slots && sub == (s & (L - 1))) {
+          const int e = slot(s, dw);
+          if (e >= 0) buf[e] += own * (dw - mean);
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    float d[V];
+    read_row<L, V>(buf, E, sub, quads, d);
+    __syncwarp();
+    if (slots)
+      for (int s = sub; s < K; s += L) {
+        const int e = slot(s, dw);
+        if (e >= 0) buf[e] = 0.0f;
+      }
+    if (SIGMOID) {
+      if (balance) {
+        const float shared = gp * z_inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = __fmaf_rn(g[i] - shared, z_inv, d[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] *= p[i] * q[i];
+    } else {
+      const float all = __fmaf_rn(own * unit, dot - mean * total, gp * unit);
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = (p[i] * unit) * (d[i] + g[i] - all);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = live ? d[i] : 0.0f;
+    if (here) store_row<L, V, T>(grad + t * E, E, sub, quads, d);
     __syncwarp();
   }
 }
@@ -795,29 +1221,41 @@ __global__ void __launch_bounds__(256) scatter_weights_kernel(const float* __res
   row_weights[r] = weights[i];
 }
 
+// Tokens a CTA takes at a time, and the CTAs of a forward launch.
+int tokens_per_cta(int experts) { return kWarps * (experts <= 64 ? 4 : experts <= 128 ? 2 : 1); }
 int router_blocks(int64_t tokens, int experts) {
-  const int64_t b = (tokens + kWarps - 1) / kWarps;
+  const int64_t b = (tokens + tokens_per_cta(experts) - 1) / tokens_per_cta(experts);
   return (int)(b < 1 ? 1 : b < max_blocks(experts) ? b : max_blocks(experts));
 }
+// Few tokens: up to eight CTAs, two rounds each, joined as one cluster - no second launch (64
+// tokens to 32 experts: 5.4 us on the GPU; four rounds, 1000 tokens, took 11.6 us, as much as
+// the second launch costs).
+constexpr int kFusedCtas = 8;
+bool fused(int64_t tokens, int experts) { return tokens <= (int64_t)2 * kFusedCtas * tokens_per_cta(experts); }
 
-template <int VPL, typename T>
-cudaError_t launch_fwd(int mode, int blocks, const T* logits, const float* bias, const uint8_t* mask,
-                       const RouterArgs& a, int32_t* idx, float* weights, uint32_t* ws, cudaStream_t st) {
-  auto k = mode == kSoftmax ? router_kernel<VPL, kSoftmax, T>
-                            : mode == kSigmoid ? router_kernel<VPL, kSigmoid, T> : router_kernel<VPL, kSigmoidBias, T>;
-  return launch_after(k, dim3((unsigned)blocks), kThreads, 0, st, logits, bias, mask, a, idx, weights, ws);
-}
+struct FwdPtrs {
+  const float* bias;
+  const uint8_t* mask;
+  int32_t* idx;
+  float* weights;
+};
 
 template <typename T>
-cudaError_t launch_fwd_for(int mode, int blocks, const void* logits, const float* bias, const uint8_t* mask,
-                           const RouterArgs& a, int32_t* idx, float* weights, uint32_t* ws, cudaStream_t st) {
-  const T* l = static_cast<const T*>(logits);
-  if (a.E <= 32) return launch_fwd<1>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
-  if (a.E <= 64) return launch_fwd<2>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
-  if (a.E <= 128) return launch_fwd<4>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
-  if (a.E <= 256) return launch_fwd<8>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
-  if (a.E <= 512) return launch_fwd<16>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
-  return launch_fwd<32>(mode, blocks, l, bias, mask, a, idx, weights, ws, st);
+cudaError_t launch_fwd(int mode, const T* logits, const FwdPtrs& p, const RouterArgs& a, const StatsOut& out, int blocks,
+                       cudaStream_t st) {
+  using Kernel = void (*)(const T*, const float*, const uint8_t*, RouterArgs, int32_t*, float*, StatsOut);
+#define FP8Q_BY_MODE(name, ...) \
+  (mode == kSoftmax ? (Kernel)name<__VA_ARGS__, kSoftmax, T> \
+                    : mode == kSigmoid ? (Kernel)name<__VA_ARGS__, kSigmoid, T> : (Kernel)name<__VA_ARGS__, kSigmoidBias, T>)
+  const Kernel k = a.E <= 32    ? FP8Q_BY_MODE(router_small_kernel, 8, 4)
+                   : a.E <= 64  ? FP8Q_BY_MODE(router_small_kernel, 8, 8)
+                   : a.E <= 128 ? FP8Q_BY_MODE(router_small_kernel, 16, 8)
+                   : a.E <= 256 ? FP8Q_BY_MODE(router_kernel, 8)
+                   : a.E <= 512 ? FP8Q_BY_MODE(router_kernel, 16)
+                                : FP8Q_BY_MODE(router_kernel, 32);
+#undef FP8Q_BY_MODE
+  return launch_clusters_after(k, (unsigned)blocks, out.fused ? (unsigned)blocks : 1u, kThreads, 0, st, logits, p.bias,
+                               p.mask, a, p.idx, p.weights, out);
 }
 
 struct BwdPtrs {
@@ -831,28 +1269,23 @@ struct BwdPtrs {
   const float* grad_loss;
 };
 
-template <int VPL, typename T>
+template <typename T>
 cudaError_t launch_bwd(bool sigmoid, const T* logits, const RouterArgs& a, const BwdPtrs& p, T* grad, int* status,
                        cudaStream_t st) {
-  auto k = sigmoid ? router_bwd_kernel<VPL, true, T> : router_bwd_kernel<VPL, false, T>;
-  const int64_t need = (a.tokens + kWarps - 1) / kWarps, most = 148 * resident_bwd(VPL);
-  const int64_t blocks = need < most ? need : most;
-  const size_t smem = (size_t)(kWarps + 1) * ((a.E + 3) & ~3) * sizeof(float);  // at most 36 KB
-  return launch_after(k, dim3((unsigned)blocks), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
+  using Kernel = void (*)(const T*, const uint8_t*, RouterArgs, const int32_t*, const float*, const int32_t*, int64_t,
+                          const int32_t*, float, const float*, T*, int*);
+#define FP8Q_BY_MODE(name, ...) (sigmoid ? (Kernel)name<__VA_ARGS__, true, T> : (Kernel)name<__VA_ARGS__, false, T>)
+  const Kernel k = a.E <= 32    ? FP8Q_BY_MODE(router_small_bwd_kernel, 8, 4)
+                   : a.E <= 64  ? FP8Q_BY_MODE(router_small_bwd_kernel, 8, 8)
+                   : a.E <= 128 ? FP8Q_BY_MODE(router_small_bwd_kernel, 16, 8)
+                   : a.E <= 256 ? FP8Q_BY_MODE(router_bwd_kernel, 8)
+                   : a.E <= 512 ? FP8Q_BY_MODE(router_bwd_kernel, 16)
+                                : FP8Q_BY_MODE(router_bwd_kernel, 32);
+#undef FP8Q_BY_MODE
+  // The larger kernel's g_e and a row per warp: at most 36 KB.
+  const size_t smem = a.E <= 128 ? 0 : (size_t)(kWarps + 1) * ((a.E + 3) & ~3) * sizeof(float);
+  return launch_after(k, dim3((unsigned)router_blocks(a.tokens, a.E)), kThreads, smem, st, logits, p.mask, a, p.idx, p.gw,
                       p.map, p.rows, p.counts, p.loss_coef, p.grad_loss, grad, status);
-}
-
-template <typename T>
-cudaError_t launch_bwd_for(bool sigmoid, const void* logits, const RouterArgs& a, const BwdPtrs& p, void* grad,
-                           int* status, cudaStream_t st) {
-  const T* l = static_cast<const T*>(logits);
-  T* g = static_cast<T*>(grad);
-  if (a.E <= 32) return launch_bwd<1>(sigmoid, l, a, p, g, status, st);
-  if (a.E <= 64) return launch_bwd<2>(sigmoid, l, a, p, g, status, st);
-  if (a.E <= 128) return launch_bwd<4>(sigmoid, l, a, p, g, status, st);
-  if (a.E <= 256) return launch_bwd<8>(sigmoid, l, a, p, g, status, st);
-  if (a.E <= 512) return launch_bwd<16>(sigmoid, l, a, p, g, status, st);
-  return launch_bwd<32>(sigmoid, l, a, p, g, status, st);
 }
 
 constexpr uint32_t kKnownFlags = FP8Q_ROUTER_SIGMOID | FP8Q_ROUTER_RENORM | FP8Q_ROUTER_BF16;
@@ -875,6 +1308,7 @@ extern "C" {
 
 size_t fp8q_router_workspace_bytes(int64_t tokens, int32_t num_experts) {
   if (tokens < 0 || num_experts < 1 || num_experts > kRouterMaxExperts) return 0;
+  if (fused(tokens, num_experts)) return 16;
   return 16 + (size_t)router_blocks(tokens, num_experts) * num_experts * 8;
 }
 
@@ -901,20 +1335,22 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
   if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
   const RouterArgs a = {tokens, num_experts, topk, (flags & FP8Q_ROUTER_RENORM) != 0, stats, scale};
   const int mode = !(flags & FP8Q_ROUTER_SIGMOID) ? kSoftmax : bias ? kSigmoidBias : kSigmoid;
-  const int blocks = router_blocks(tokens, num_experts);
-  uint32_t* ws = stats ? static_cast<uint32_t*>(workspace) : nullptr;
   cudaStream_t st = to_stream(stream);
+  const bool one = stats && fused(tokens, num_experts);
+  int blocks = router_blocks(tokens, num_experts);
+  if (one && blocks > kFusedCtas) blocks = kFusedCtas;
+  const StatsOut out = {static_cast<uint32_t*>(workspace), counts, prob_sums, loss, loss_coef, one};
+  const FwdPtrs p = {bias, token_mask, topk_idx, weights};
   const cudaError_t rc =
       (flags & FP8Q_ROUTER_BF16)
-          ? launch_fwd_for<uint16_t>(mode, blocks, logits, bias, token_mask, a, topk_idx, weights, ws, st)
-          : launch_fwd_for<float>(mode, blocks, logits, bias, token_mask, a, topk_idx, weights, ws, st);
+          ? launch_fwd(mode, static_cast<const uint16_t*>(logits), p, a, out, blocks, st)
+          : launch_fwd(mode, static_cast<const float*>(logits), p, a, out, blocks, st);
   if (rc != cudaSuccess) return FP8Q_ERR_CUDA;
-  if (!stats) return FP8Q_OK;
+  if (!stats || one) return FP8Q_OK;
   // Few rows need no cluster: 64 are one or two a warp.
   const unsigned size = blocks > 64 ? kFinishCluster : blocks > kWarps ? 2 : 1;
   return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st,
-                               blocks, (int)num_experts, (int)topk, loss_coef, ws, counts, prob_sums,
-                               loss) == cudaSuccess
+                               blocks, a, out) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }
@@ -938,8 +1374,10 @@ fp8q_status fp8q_router_topk_bwd(const void* logits, int64_t tokens, int32_t num
   const BwdPtrs p = {token_mask, topk_idx, grad_weights, row_id_map, grad_rows, counts, loss_coef, grad_loss};
   const bool sigmoid = (flags & FP8Q_ROUTER_SIGMOID) != 0;
   const cudaError_t rc = (flags & FP8Q_ROUTER_BF16)
-                             ? launch_bwd_for<uint16_t>(sigmoid, logits, a, p, grad_logits, dev.status, to_stream(stream))
-                             : launch_bwd_for<float>(sigmoid, logits, a, p, grad_logits, dev.status, to_stream(stream));
+                             ? launch_bwd(sigmoid, static_cast<const uint16_t*>(logits), a, p,
+                                          static_cast<uint16_t*>(grad_logits), dev.status, to_stream(stream))
+                             : launch_bwd(sigmoid, static_cast<const float*>(logits), a, p,
+                                          static_cast<float*>(grad_logits), dev.status, to_stream(stream));
   return rc == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
 }
 

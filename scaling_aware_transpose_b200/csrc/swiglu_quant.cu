@@ -45,6 +45,8 @@
 // codes (fp8q_swiglu_bwd, swiglu_bwd.cu), quantized by the same 1x128 rule from the registers
 // that already hold them: 2 B of writes and no read per element.  Row-wise only, so a warp
 // walks runs of four tiles that lie contiguously in memory, the next run's loads in flight.
+// [32768, 2048]: 87 us for 7 B an element, 5.4 TB/s (as a variant of the block loop above, with
+// its 128 x 128 blocks: 107 us; quantizing gate and up by calls of their own: 61 + 2 x 33 us).
 #include "abi_checks.h"
 #include "common.cuh"
 #include "launch.h"

@@ -21,7 +21,7 @@ def test_router_refusals(L):
         return L.fp8q_router_topk(logits, T, E, flags, bias, mask, K, 1.0, 1.0, idx, w, counts, sums, loss, ws, n, None)
 
     for kw in (dict(E=0), dict(E=1025), dict(K=0), dict(K=33), dict(E=1024, K=65), dict(flags=8), dict(bias=A),
-               dict(counts=None), dict(sums=None), dict(loss=None), dict(n=100)):
+               dict(counts=None), dict(sums=None), dict(loss=None), dict(n=10), dict(T=100000, n=100)):
         assert f(**kw) == sat.FP8Q_ERR_ARG, kw
     for kw in (dict(T=-1), dict(T=1 << 40)):
         assert f(**kw) == sat.FP8Q_ERR_SHAPE, kw
@@ -31,7 +31,7 @@ def test_router_refusals(L):
         assert f(**kw) == sat.FP8Q_ERR_ALIGN, kw
     assert f(T=0, logits=None, idx=None, w=None, counts=None, sums=None, loss=None, ws=None) == sat.FP8Q_OK
     assert sat.fp8q_router_workspace_bytes(-1, 8) == 0 and sat.fp8q_router_workspace_bytes(4, 2000) == 0
-    assert sat.fp8q_router_workspace_bytes(0, 32) >= 32 * 8
+    assert sat.fp8q_router_workspace_bytes(0, 32) >= 16 and sat.fp8q_router_workspace_bytes(1 << 20, 32) >= 32 * 8
 
 
 def test_router_bwd_refusals(L):
