@@ -368,7 +368,8 @@ fp8q_status fp8q_permute_pad_quant_noalloc(const void *x, int64_t tokens, int64_
  *                an expert off (p = 0; it is chosen only when fewer than topk others are
  *                left, with weight 0).  NaN counts as -inf, +inf as the largest finite
  *                value.  A row of -inf alone gets ids 0..topk-1 with weights 0.
- *   bias       : fp32 [num_experts], only with FP8Q_ROUTER_SIGMOID, or NULL.
+ *   bias       : fp32 [num_experts], only with FP8Q_ROUTER_SIGMOID, or NULL.  A score p + bias
+ *                that is NaN counts as -inf.
  *   token_mask : u8 [tokens] or NULL.  A token with 0 (padding) still gets valid ids, its
  *                weights are 0, and it takes no part in the statistics and the gradient.
  *   topk_idx   : out int32 [tokens, topk];  weights : out fp32 [tokens, topk].

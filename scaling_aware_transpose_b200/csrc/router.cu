@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
         float order[VPL];
         load_row<32, VPL, float>(bias, E, lane, quads && bias_quads, order);  // (padding lanes: -inf)
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) order[i] += p[i];
+        for (int i = 0; i < VPL; ++i) order[i] = fmaxf(order[i] + p[i], -INFINITY);  // (NaN counts as -inf)
         done = pick_listed<VPL, MODE>(order, val, bias, K, lane, picks);
       } else {
         done = pick_listed<VPL, MODE>(val, val, bias, K, lane, picks);

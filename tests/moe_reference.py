@@ -28,6 +28,7 @@ def router(logits, topk, sigmoid=False, renorm=True, bias=None, mask=None, scale
             p = x / np.where(z == 0, 1.0, z)
             h = p
     key = p + np.asarray(bias, np.float64) if bias is not None else l
+    key = np.where(np.isnan(key), -np.inf, key)
     idx = np.argsort(-key, axis=1, kind="stable")[:, :topk]
     pk = np.take_along_axis(p, idx, 1)
     P = pk.sum(1, keepdims=True) + 1e-20 if renorm else np.ones((T, 1))

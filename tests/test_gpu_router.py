@@ -74,15 +74,16 @@ def test_token_counts(T):
     check(make(T, 72, T), 6, sigmoid=True, bias=torch.randn(72, generator=torch.Generator().manual_seed(3)) * 0.1)
 
 
-def test_ties_take_the_lowest_id():
-    l = torch.zeros((5, 100))
+@pytest.mark.parametrize("E", [100, 140, 300, 1024])
+def test_ties_take_the_lowest_id(E):
+    l = torch.zeros((5, E))
     l[1, ::2] = -0.0
     l[2, 50:] = 1.0
-    l[3] = torch.arange(100).flip(0) // 10
+    l[3] = torch.arange(E).flip(0) // 10
     idx = check(l, 12)[0].cpu()
     assert idx[0].tolist() == list(range(12)) and idx[1].tolist() == list(range(12))
     assert idx[2].tolist() == list(range(50, 62))
-    check(l, 12, sigmoid=True, bias=torch.zeros(100))
+    check(l, 12, sigmoid=True, bias=torch.zeros(E))
 
 
 def test_bias_ties_below_fp32_resolution():
@@ -96,8 +97,9 @@ def test_bias_ties_below_fp32_resolution():
     check(torch.zeros((3, E)), 9, sigmoid=True, bias=torch.randn(E, generator=g))
 
 
-def test_switched_off_masked_and_empty_rows():
-    T, E, K = 301, 60, 6
+@pytest.mark.parametrize("E", [60, 128, 160, 320, 1000])
+def test_switched_off_masked_and_empty_rows(E):
+    T, K = 301, 6
     l = make(T, E, 11)
     l[:, 7] = -float("inf")
     l[5] = -float("inf")             # nothing left
@@ -118,6 +120,27 @@ def test_switched_off_masked_and_empty_rows():
     m = torch.zeros(T, dtype=torch.bool)
     _, w, counts, sums, loss = check(l, K, mask=m)      # every token masked
     assert float(loss) == 0.0 and int(counts.sum()) == 0 and (sums == 0).all() and (w == 0).all()
+
+
+@pytest.mark.parametrize("E,K", [(40, 8), (128, 8), (256, 8), (256, 20), (320, 12), (1024, 16)])
+def test_bias_that_is_not_finite(E, K):
+    """A NaN bias counts as -inf, whole lanes of them (neighbours in fours) and all of them
+    included; +inf puts an expert first."""
+    l = make(50, E, E)
+    nan = float("nan")
+    for where in (slice(0, 4), slice(0, E, 3), slice(0, E - 1), slice(0, E)):
+        bias = torch.linspace(-0.2, 0.2, E)
+        bias[where] = nan
+        check(l, K, sigmoid=True, bias=bias)
+    groups = (torch.arange(E) // 4) % 32 < 6     # every expert of six lanes
+    check(l, K, sigmoid=True, bias=torch.linspace(-0.2, 0.2, E).masked_fill(groups, nan))
+    shifted = torch.linspace(-0.2, 0.2, E + 1).cuda()[1:]        # not on 16 bytes
+    a = sat.router_topk(l.cuda(), K, sigmoid=True, bias=shifted, balance=False)
+    b = sat.router_topk(l.cuda(), K, sigmoid=True, bias=shifted.clone(), balance=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    bias = torch.linspace(-0.2, 0.2, E)
+    bias[E // 2], bias[E // 3], bias[7] = float("inf"), float("inf"), -float("inf")
+    assert (check(l, K, sigmoid=True, bias=bias)[0][:, :2].cpu() == torch.tensor([E // 3, E // 2])).all()
 
 
 def test_no_tokens():
@@ -159,8 +182,9 @@ def test_gradient_against_differences(sigmoid, renorm):
     near(got.cpu(), want, 4 * router_units(l64) * U * mag + 1e-8, "gradient")
 
 
-def test_row_order_gradient_and_row_weights():
-    T, E, K, align = 203, 16, 4, 16
+@pytest.mark.parametrize("E", [16, 48, 100, 200, 600])
+def test_row_order_gradient_and_row_weights(E):
+    T, K, align = 203, 4, 16
     l = make(T, E, 31)
     idx, w, counts, _, _ = sat.router_topk(l.cuda(), K)
     x = torch.randn((T, 128), device="cuda").to(torch.bfloat16)
@@ -185,10 +209,10 @@ def test_row_order_gradient_and_row_weights():
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("K", [8, 40])
-def test_repeated_and_bad_ids_in_the_backward(K):
+@pytest.mark.parametrize("E,K", [(32, 8), (64, 8), (64, 40), (128, 33), (200, 8), (256, 40), (600, 40)])
+def test_repeated_and_bad_ids_in_the_backward(E, K):
     """Ids that a caller made: a repeated one adds up, one out of range is skipped."""
-    T, E = 9, 64
+    T = 9
     l = make(T, E, 41)
     idx = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:K] for t in range(T)]).int()
     idx[0] = 5
@@ -203,10 +227,11 @@ def test_repeated_and_bad_ids_in_the_backward(K):
     assert sat.fp8q_last_device_status() == sat.FP8Q_ERR_DEVICE
 
 
-def test_same_bits_every_time_and_under_capture():
+@pytest.mark.parametrize("E", [64, 256])
+def test_same_bits_every_time_and_under_capture(E):
     """Two runs, two streams with their own workspaces, and a captured and replayed step on
     new inputs give the same bits."""
-    T, E, K = 20011, 64, 6
+    T, K = 20011, 6
     a, b = make(T, E, 51).cuda(), make(T, E, 52).cuda()
     gl, gw = torch.ones(1, device="cuda"), torch.randn((T, K), device="cuda")
 
