@@ -19,7 +19,7 @@
 // memory by bulk copies 140 us, one-shot CTAs with the loads in front 119 us).
 // The codes' scales stay out of the arithmetic (g = sg g', u = su u' with the raw codes' values
 // g', u'; the factors sg, su, w meet once per tile):
-//   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + (a sg)(1 - s),  x = dy u'
+//   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + a (1 - s) sg,  x = dy u'
 //   d gate = x slope (w su),  d up = dy a (w sg),  y = a u' (w sg su),  d w += x a (sg su).
 #include "abi_checks.h"
 #include "common.cuh"
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, Fp8 ? 5 : 6) swiglu_bwd_kernel(BwdIn
       split2(add2(make2(ex2(e0), ex2(e1)), one), e0, e1);
       const F2 s = make2(rcp(e0), rcp(e1));
       const F2 act = mul2(g, s);
-      const F2 slope = fma2(mul2(act, sg2), fma2(s, minus, one), s);
+      const F2 slope = fma2(mul2(act, fma2(s, minus, one)), sg2, s);  // (a sg alone can overflow)
       const F2 x = mul2(d, u);
       dg[k] = mul2(x, slope);
       du[k] = mul2(d, act);

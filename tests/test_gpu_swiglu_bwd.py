@@ -127,6 +127,20 @@ def test_backward_at_the_edges():
     check(gq, gsf, uq, usf, dy, w)
 
 
+def test_largest_gates():
+    """The largest BF16 gate: its code's value is 2^128, beyond fp32, yet sigmoid' there is 0 and
+    the gate's gradient is dy * up (and 0 for the negative one)."""
+    gate = torch.ones((2, 128), dtype=torch.bfloat16)
+    gate[0, :64], gate[0, 64:] = torch.finfo(torch.bfloat16).max, torch.finfo(torch.bfloat16).min
+    up, dy = torch.full_like(gate, 1.5), torch.full_like(gate, 0.5)
+    _, _, *s = sat.swiglu_quant_stash(gate.cuda(), up.cuda())
+    dg = sat.swiglu_bwd(*s, dy.cuda())[0]
+    assert (dg[0, :64] == 0.75).all() and (dg[0, 64:] == 0).all()
+    dgq, dgsf, *_ = sat.swiglu_bwd_quant(*s, dy.cuda(), recompute=False)
+    assert np.array_equal(decode8(dgq.cpu().numpy(), dgsf.cpu().numpy())[0], [0.75] * 64 + [0.0] * 64)
+    device_status_ok()
+
+
 def test_no_rows_no_columns():
     u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device="cuda")  # noqa: E731
     dg, _, dw = sat.swiglu_bwd(u8(0, 256), u8(0, 2), u8(0, 256), u8(0, 2),
