@@ -14,7 +14,7 @@
 //   warps 2-9  scales: shared memory -> registers -> tensor memory, each warp its quarter of
 //              the lanes, two warps a quarter taking turns.  (tcgen05.cp from the MMA thread
 //              took turns with the MMAs: 36 ns a 512-byte tile, and the pipe drained at each
-//              change from one to the other: 141 us for what now takes 105.)
+//              change from one to the other: 141 us for what took 105 this way.)
 //   warps 10-13  the epilogue: tensor memory -> registers -> BF16 -> global.
 // What bounds it: at large sizes the tensor pipe and the 1000 W power cap (below, CTA pairs);
 // at few rows the chain of a CTA's stages, about 0.3 us each, on top of 3 us of start, first
@@ -194,14 +194,22 @@ __device__ __forceinline__ bool wait_or_record(uint64_t* bar, uint32_t parity, i
 
 // One epilogue warp: 32 rows (row0 + lane) x BN columns of the accumulator at `tmem` to BF16
 // rows of out below row_end and columns below n.  `read` is called once the accumulator has
-// been read to the end.
-template <int BN, typename Read>
+// been read to the end: kPart columns are packed in registers at a time, all of a pair's, whose
+// one accumulator the next tile waits for, and 64 of a CTA's alone (128 at a time spilled in the
+// 256-column kernel: 1024x4096x4096 12.7 us, not 11.5).
+//
+// Where rows start on 16 bytes the words pass through shared memory, eight rows of 64 columns at
+// a time (16-byte pieces, their order within a row exchanged by its number: no bank conflicts),
+// so that a store instruction covers whole 128-byte runs, in 32-byte stores where rows start on
+// 32 bytes.  The stores share the path between the SMs and L2 with the operands, which at large
+// sizes take some 48 bytes a cycle of each SM: 8192x4096x7168 takes 86 us so, 89 with each lane
+// storing its own row in 32-byte pieces, 96 in 16-byte pieces, 79 without stores.
+template <int BN, int kPart, typename Read>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, uint32_t tmem, int64_t row0, int64_t row_end, int64_t col,
-                                           bool vec, int lane, uint32_t* staging, Read read) {
-  const int64_t r = row0 + lane;
-  uint16_t* dst = a.out + r * a.n + col;
+                                           int lane, uint32_t* staging, Read read) {
+  const bool aligned = (a.n & 7) == 0;
+  const bool wide = (a.n & 15) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   const int left = (int)min((int64_t)BN, a.n - col);  // columns of this tile that exist
-  constexpr int kPart = BN < 128 ? BN : 128;          // columns packed in registers at a time
 #pragma unroll 1
   for (int h = 0; h < BN; h += kPart) {
     uint32_t p[kPart / 2];
@@ -214,17 +222,43 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, uint32_t tmem, i
       for (int i = 0; i < 16; ++i) p[c / 2 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
     if (h + kPart == BN) read();  // the next tile's MMAs may overwrite it
-    if (vec) {
-      if (r < row_end) {
+    if (aligned) {
+      constexpr int kWide = kPart < 64 ? kPart : 64, kPieces = kWide / 8, kRowLanes = kWide / 16, kRows = 32 / kRowLanes;
+      uint4* st = reinterpret_cast<uint4*>(staging);
+      const int sr = lane / kRowLanes, sq = 2 * (lane % kRowLanes), turn = sr & (kPieces - 1);
 #pragma unroll
-        for (int c = 0; c < kPart; c += 8)
-          if (h + c < left)
-            *reinterpret_cast<uint4*>(dst + h + c) = make_uint4(p[c / 2], p[c / 2 + 1], p[c / 2 + 2], p[c / 2 + 3]);
+      for (int c = 0; c < kPart; c += kWide) {
+#pragma unroll 1
+        for (int g = 0; g < 32; g += kRows) {
+          if (lane / kRows * kRows == g) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+              st[(lane - g) * kPieces + (i ^ (lane & (kPieces - 1)))] =
+                  make_uint4(p[c / 2 + 4 * i], p[c / 2 + 4 * i + 1], p[c / 2 + 4 * i + 2], p[c / 2 + 4 * i + 3]);
+          }
+          __syncwarp();
+          const uint4 lo = st[sr * kPieces + (sq ^ turn)], hi = st[sr * kPieces + ((sq + 1) ^ turn)];
+          const int64_t r = row0 + g + sr;
+          const int x = h + c + 8 * sq;
+          if (r < row_end && x < left) {
+            uint16_t* to = a.out + r * a.n + col + x;
+            if (wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(lo.x), "r"(lo.y),
+                           "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(to) = lo;
+              if (x + 8 < left) *reinterpret_cast<uint4*>(to + 8) = hi;
+            }
+          }
+          __syncwarp();
+        }
       }
     } else {
-      // Rows that do not start on 16 bytes: 16 columns at a time through shared memory, so
-      // that half a warp stores 16 neighbouring elements of a row (each lane storing its own
-      // row element by element took 2.5 times as long over the whole product).
+      // Other rows: 16 columns at a time, so that half a warp stores 16 neighbouring elements of
+      // a row, with all of a chunk's loads on their way before its stores (1003x2050x1408: 7.9 us,
+      // 9.1 in rounds of four; each lane storing its own row element by element took 2.5 times
+      // as long over the whole product).
       uint32_t* mine = staging + lane * kPitch;
       const uint16_t* all = reinterpret_cast<const uint16_t*>(staging);
       const int rows_here = (int)max((int64_t)0, min((int64_t)32, row_end - row0));
@@ -232,12 +266,17 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, uint32_t tmem, i
 #pragma unroll
       for (int c = 0; c < kPart; c += 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i] = p[c / 2 + i];
+        for (int i = 0; i < 8; ++i) mine[i ^ (lane >> 2)] = p[c / 2 + i];
         __syncwarp();
         const int x = c + (lane & 15);
+        uint16_t* to = base + (lane >> 4) * a.n + x;
         if (h + x < left) {
-#pragma unroll 4
-          for (int i = lane >> 4; i < rows_here; i += 2) base[i * a.n + x] = all[i * 2 * kPitch + (lane & 15)];
+#pragma unroll 16
+          for (int i = 0; i < 32; i += 2) {
+            const int r = i + (lane >> 4);
+            if (r < rows_here) *to = all[(r * kPitch + ((lane >> 1 & 7) ^ (r >> 2))) * 2 + (lane & 1)];
+            to += 2 * a.n;
+          }
         }
         __syncwarp();
       }
@@ -253,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], scaled[STAGES], sf_full[kSfSlots], sf_empty[kSfSlots];
   __shared__ uint64_t acc_full[C::kAcc], acc_empty[C::kAcc], drain;
-  __shared__ uint32_t tmem_sh, odd_rows[4][32 * kPitch];
+  __shared__ uint32_t tmem_sh;
+  __shared__ __align__(16) uint32_t odd_rows[4][32 * kPitch];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -480,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;  // the tensor-memory lanes this warp may read
     int acc = 0;
     uint32_t acc_phase = 0;
-    const bool vec = (a.n & 7) == 0;
     for (int64_t t = t0; t < tiles; t += stride) {
       Tile o;
       if (!locate(a, t, n_tiles, BN, o)) continue;
@@ -504,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         break;
       }
-      store_tile<BN>(a, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN, o.row + quad * 32, rows, o.col, vec, lane,
+      store_tile<BN, (BN < 64 ? BN : 64)>(a, tmem + ((uint32_t)(quad * 32) << 16) + acc * BN, o.row + quad * 32, rows, o.col, lane,
                      odd_rows[quad], [&] {
                        tc_fence_before();
                        __syncwarp();
@@ -615,9 +654,9 @@ fp8q_status launch_matmul(const DeviceInfo& dev, const uint8_t* aq, const uint8_
 // of A and of B (half the B bytes of a CTA alone) and holds 128 rows of the accumulator; the
 // first one's MMAs (cta_group::2, M = 256) read both.  A CTA alone at 128 x 256 moves 48 KB of
 // codes into shared memory and 48 KB out per stage, more than the 128 bytes a cycle allow
-// under the MMAs; a pair moves 32 KB each way: 475 cycles a stage against 955.  At 8192^3 it
-// runs at 5.2 PFLOP/s for the first milliseconds and at 4.65 under the 1000 W cap, which
-// takes the SM clock to 1.55 GHz (a CTA alone there: 4.25).
+// under the MMAs; a pair moves 32 KB each way.  8192x4096x7168: 86 us, 102 by CTAs alone; 8192^3:
+// 190 us (5.8 PFLOP/s) for the first milliseconds and 210 us under the 1000 W cap, which takes
+// the SM clock to 1.36 GHz.
 // What the pair exchanges: the copies of both complete on the first CTA's `full`; the second
 // one's scale warps and epilogue arrive on the first one's `scaled` and `acc_empty`; warp 18 of
 // the first CTA passes `empty` and `acc_full`, which the MMAs' commits set, on to the second.
@@ -648,7 +687,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kPairStages], empty[kPairStages], scaled[kPairStages], sf_full[kSfSlots], sf_empty[kSfSlots];
   __shared__ uint64_t acc_full, acc_empty, drain;
-  __shared__ uint32_t tmem_sh, odd_rows[8][32 * kPitch];
+  __shared__ uint32_t tmem_sh;
+  __shared__ __align__(16) uint32_t odd_rows[8][32 * kPitch];
   __shared__ int tiles_before[kPairMaxGroups + 1];  // of 256 rows, in the groups before g
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -899,15 +939,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp < 18) {
     const int quad = warp & 3, half = (warp - 10) >> 2;  // a quarter of the rows, half of the columns
     uint32_t acc_phase = 0;
-    const bool vec = (a.n & 7) == 0;
     for (int64_t t = t0; t < tiles; t += stride) {
       const PairTile o = locate_pair(t);
       if (!wait_or_record(&acc_full, acc_phase, a.status)) break;
       acc_phase ^= 1u;
       tc_fence_after();
       const int64_t row0 = o.row + rank * kBM + quad * 32;
-      store_tile<kPairN / 2>(a, tmem + ((uint32_t)(quad * 32) << 16) + half * (kPairN / 2), row0, o.row_end,
-                             o.col + half * (kPairN / 2), vec, lane, odd_rows[warp - 10], [&] {
+      store_tile<kPairN / 2, kPairN / 2>(a, tmem + ((uint32_t)(quad * 32) << 16) + half * (kPairN / 2), row0, o.row_end,
+                             o.col + half * (kPairN / 2), lane, odd_rows[warp - 10], [&] {
                                tc_fence_before();
                                __syncwarp();
                                if (lane == 0) arrive_at(peer_address(smem_u32(&acc_empty), 0));
@@ -973,10 +1012,14 @@ fp8q_status launch_pair(const DeviceInfo& dev, const uint8_t* aq, const uint8_t*
 //   the tile's stored elements (1x4096x7168: 11.3 us unshared at 64 columns, 7.0 us with 4
 //   CTAs at 128; 256x4096x4096: 7.9 us unshared at 64, 9.1 us with 2 at 128).  It is taken
 //   within one wave only, where the clusters are resident together;
+//   rows of out that do not start on 16 bytes take longer to store: 0.11 ns for each element of
+//   a tile, by a pair 0.7 us (1003x2050x1408: 7.7 us at 128, 8.9 by pairs; 1500x2050x2048: 12.6 at
+//   128, 10.2 by pairs);
 //   a pair's stage takes 330 ns for twice the rows, its start 3.1 us more than a CTA's alone,
-//   a change of tiles 0.7 us (8192x4096x7168: 96 us against 105 us; 2048x4096x4096: 21.2
-//   against 21.4; 1024x4096x4096: 12.7 against 11.3).  With groups, the last 256 rows of each
-//   may be half empty: pairs are left to groups of 512 rows on average.
+//   a change of tiles 0.7 us (8192x4096x7168: 86 us against 102 us at 256; 2048x4096x4096: 18.2
+//   against 21.8; 1024x4096x4096: 11.9 both; 512x4096x4096: 11.2 against 9.3 at 128).  With
+//   groups, the last 256 rows of each may be half empty: pairs are left to groups of 512 rows on
+//   average.
 struct Variant {
   int bn, split;  // bn 0: pairs
 };
@@ -992,7 +1035,9 @@ Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sm
       if (s > 1 && (tiles * s > sms || s > steps || kBn[i] == 32)) break;
       const double waves = (double)((tiles * s + sms - 1) / sms);
       double t = waves * (double)((steps + s - 1) / s) * kStage[i] + 4.0 * kBn[i] * (i == 0 ? waves : 1.0);
-      if (s > 1) t += 1200 + 0.12 * (double)(m < kBM ? m : kBM) * kBn[i];
+      const double stored = (double)(m < kBM ? m : kBM) * kBn[i];  // of a tile
+      if (s > 1) t += 1200 + 0.12 * stored;
+      else if (n % 8) t += waves * 0.11 * stored;
       if (t < least) {
         least = t;
         best = {kBn[i], s};
@@ -1002,7 +1047,7 @@ Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sm
   if (!grouped || (groups <= kPairMaxGroups && m >= 512 * (int64_t)groups)) {
     const int64_t tiles = (m + 2 * kBM - 1) / (2 * kBM) * ((n + kPairN - 1) / kPairN);
     const double waves = (double)((tiles + sms / 2 - 1) / (sms / 2));
-    if (3100 + waves * ((double)steps * 330 + 700) < least) best = {0, 1};
+    if (3100 + waves * ((double)steps * 330 + (n % 8 ? 1400 : 700)) < least) best = {0, 1};
   }
   return best;
 }

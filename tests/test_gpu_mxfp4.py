@@ -169,7 +169,9 @@ def test_product_large(m, n, k):
 @pytest.mark.parametrize("m,n,k", [(2, 4821, 128), (130, 2048, 1152), (61, 2467, 3456), (40, 2560, 3456), (5, 67, 1664),
                                    (128, 200, 3200), (2, 10885, 384), (300, 5120, 640), (2, 5597, 3456), (7, 5600, 3456),
                                    (2, 2469, 1920), (100, 2472, 1920), (131, 9690, 640), (256, 9728, 896),
-                                   (2, 9735, 4992), (90, 9736, 4992), (2, 4884, 2944), (128, 4888, 2944)])
+                                   (2, 9735, 4992), (90, 9736, 4992), (2, 4884, 2944), (128, 4888, 2944),
+                                   (260, 9517, 640), (148, 9512, 640), (1, 10168, 6400), (3, 10016, 6400),
+                                   (1, 6464, 2944), (79, 2720, 3584), (65, 2398, 3200), (1003, 2050, 640)])
 def test_product_by_every_tile_width(m, n, k):
     """Sizes on either side of 16-byte rows for each tile width, alone and with k shared by two
     or four CTAs (odd numbers of scale tiles among them)."""
@@ -177,11 +179,24 @@ def test_product_by_every_tile_width(m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(2048, 4096, 4096), (2001, 4001, 4224), (4096, 2050, 7168), (3300, 3584, 2176),
-                                   (2561, 2560, 8192)])
+                                   (2561, 2560, 8192), (134, 10296, 4224)])
 def test_product_by_pairs(m, n, k):
     """Sizes that CTA pairs take: whole 256 x 256 tiles, a second CTA without rows, ragged
     columns, an odd number of scale tiles."""
     product(m, n, k, 2, m)
+
+
+@pytest.mark.parametrize("m,n,k", [(70, 96, 256), (300, 2048, 512), (300, 5120, 640), (260, 9520, 640), (4, 2048, 4096),
+                                   (2048, 4096, 1024), (2000, 4104, 2048)])
+def test_product_into_rows_on_16_bytes(m, n, k):
+    """Rows that start on 16 bytes but not on 32, though n is a multiple of 16 (or of 8)."""
+    aq, asf, a = operand(m, k, 1, 2)
+    bq, bsf, b = operand(n, k, 2, 2)
+    buf = torch.full((m * n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + m * n].view(m, n)
+    sat.matmul_mxfp4(aq, asf, bq, bsf, out=out)
+    assert torch.equal(out, sat.matmul_mxfp4(aq, asf, bq, bsf)) and (buf[:8] == 7.0).all() and (buf[-8:] == 7.0).all()
+    device_status_ok()
 
 
 def test_product_wide_scales_and_nan():
