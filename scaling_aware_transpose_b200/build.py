@@ -64,7 +64,7 @@ def _compile(src):
 
 def _build_binding(force: bool) -> None:
     src = os.path.join(CSRC, "moe_binding.cpp")
-    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "fp8q.h")])):
+    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__)])):
         return
     import sysconfig
 
@@ -77,7 +77,7 @@ def _build_binding(force: bool) -> None:
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(CUDA, "include"), "-isystem", sysconfig.get_paths()["include"],
            src, "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
-           "-ltorch_python", "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cuda", "-ltorch_python", "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")

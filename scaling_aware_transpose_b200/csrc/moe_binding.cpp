@@ -3,6 +3,7 @@
 // function each.  From Python these steps took 10 to 25 us a call, several times what the
 // smallest calls run on the GPU.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -36,8 +37,35 @@ struct Here {
   c10::DeviceIndex dev = c10::cuda::current_device();
   fp8q_stream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+    return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, dev), std::nullopt));
   }
+};
+
+// Small results of one call in one allocation (each takes the allocator about 1 us, more than
+// the kernels of the smallest calls spare), every part on 256 bytes: add() the parts, then make()
+// the tensors in the same order.
+class Together {
+ public:
+  explicit Together(const Here& h) : h_(h) {}
+  void add(int64_t bytes) { total_ += round_up(bytes); }
+  Tensor make(at::IntArrayRef shape, at::ScalarType type) {
+    if (!block_.defined()) block_ = h_.empty({total_}, kU8);
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block_.storage()),
+                                                        c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                        c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    const int64_t size = (int64_t)c10::elementSize(type);
+    impl->set_storage_offset(used_ / size);
+    impl->set_sizes_contiguous(shape);
+    used_ += round_up(t.numel() * size);
+    return t;
+  }
+
+ private:
+  static int64_t round_up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+  const Here& h_;
+  Tensor block_;
+  int64_t total_ = 0, used_ = 0;
 };
 
 // Address of a contiguous tensor of the type on the current device.
@@ -100,11 +128,17 @@ std::tuple<Tensor, Tensor, OptTensor, OptTensor, OptTensor> router_topk(const Te
   Tensor ws;
   size_t need = 0;
   if (balance) {
-    counts = h.empty({E}, kI32);
-    sums = h.empty({E}, kF32);
-    loss = h.empty({1}, kF32);
     need = fp8q_router_workspace_bytes(T, (int32_t)E);
-    ws = h.empty({(int64_t)need + 16}, kU8);
+    const bool few = need <= 256;  // a larger workspace is freed at the end
+    Together stats(h);
+    stats.add(4 * E);
+    stats.add(4 * E);
+    stats.add(4);
+    if (few) stats.add(256);
+    counts = stats.make({E}, kI32);
+    sums = stats.make({E}, kF32);
+    loss = stats.make({1}, kF32);
+    ws = few ? stats.make({256}, kU8) : h.empty({(int64_t)need + 16}, kU8);
   }
   check(fp8q_router_topk(l, T, (int32_t)E, flags, b, m, (int32_t)topk, (float)scale, (float)loss_coef, out<int32_t>(idx),
                          out<float>(w), out<int32_t>(counts), out<float>(sums), out<float>(loss),
@@ -154,9 +188,10 @@ Tensor permute_row_weights(const Tensor& weights, const Tensor& row_id_map, int6
   return o;
 }
 
-// Codes [rows, cols] and scales [rows, cols/128] of a row-wise pair.
-std::pair<Tensor, Tensor> pair_of(int64_t rows, int64_t cols, const Here& h) {
-  return {h.empty({rows, cols}, kU8), h.empty({rows, cols / 128}, kU8)};
+// Codes [rows, cols] and scales [rows, cols/128] of a row-wise pair; the scales of a call's pairs
+// lie together.
+std::pair<Tensor, Tensor> pair_of(int64_t rows, int64_t cols, const Here& h, Together& scales) {
+  return {h.empty({rows, cols}, kU8), scales.make({rows, cols / 128}, kU8)};
 }
 
 std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor> swiglu_quant_stash(const Tensor& gate, const Tensor& up,
@@ -168,9 +203,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor> swiglu_quant_stash(co
   shape(row_weights, "row_weights", {rows});
   const void *g = in(gate, "gate", kBF16, h), *u = in(up, "up", kBF16, h);
   const float* w = in<float>(row_weights, "row_weights", kF32, h);
-  auto [q, sf] = pair_of(rows, cols, h);
-  auto [gq, gsf] = pair_of(rows, cols, h);
-  auto [uq, usf] = pair_of(rows, cols, h);
+  Together scales(h);
+  for (int i = 0; i < 3; ++i) scales.add(rows * (cols / 128));
+  auto [q, sf] = pair_of(rows, cols, h, scales);
+  auto [gq, gsf] = pair_of(rows, cols, h, scales);
+  auto [uq, usf] = pair_of(rows, cols, h, scales);
   check(fp8q_swiglu_quant_stash(g, u, w, rows, cols, out<uint8_t>(q), out<uint8_t>(sf), out<uint8_t>(gq),
                                 out<uint8_t>(gsf), out<uint8_t>(uq), out<uint8_t>(usf), h.stream),
         "fp8q_swiglu_quant_stash");
@@ -218,15 +255,18 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, OptTensor, OptTensor, OptTensor> swig
     const OptTensor& row_weights, bool recompute) {
   const Here h;
   const BwdArgs a(gq, gsf, uq, usf, dy, row_weights, h);
-  auto [dgq, dgsf] = pair_of(a.rows, a.cols, h);
-  auto [duq, dusf] = pair_of(a.rows, a.cols, h);
+  Together small(h);
+  for (int i = 0; i < (recompute ? 3 : 2); ++i) small.add(a.rows * (a.cols / 128));
+  if (row_weights) small.add(4 * a.rows);
+  auto [dgq, dgsf] = pair_of(a.rows, a.cols, h, small);
+  auto [duq, dusf] = pair_of(a.rows, a.cols, h, small);
   OptTensor yq, ysf, dw;
   if (recompute) {
-    auto [q, sf] = pair_of(a.rows, a.cols, h);
+    auto [q, sf] = pair_of(a.rows, a.cols, h, small);
     yq = q;
     ysf = sf;
   }
-  if (row_weights) dw = h.empty({a.rows}, kF32);
+  if (row_weights) dw = small.make({a.rows}, kF32);
   check(fp8q_swiglu_bwd_quant(a.gq, a.gsf, a.uq, a.usf, a.w, a.dy, a.rows, a.cols, out<uint8_t>(dgq), out<uint8_t>(dgsf),
                               out<uint8_t>(duq), out<uint8_t>(dusf), out<uint8_t>(yq), out<uint8_t>(ysf), out<float>(dw),
                               h.stream),
@@ -260,7 +300,10 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> permute_pad_mxfp4(const Tensor& x, co
   const int32_t* idx = in<int32_t>(topk_idx, "topk_idx", kI32, h);
   const size_t need = fp8q_permute_workspace_bytes(T, (int32_t)K, (int32_t)experts);
   Tensor q = h.empty({cap, H / 2}, kU8), sf = h.empty({(int64_t)fp8q_mxfp4_sf_bytes(cap, H)}, kU8);
-  Tensor off = h.empty({experts + 1}, kI32), map = h.empty({T * K}, kI32), ws = h.empty({(int64_t)need + 16}, kU8);
+  Together routing(h);
+  routing.add(4 * (experts + 1));
+  routing.add(4 * T * K);
+  Tensor off = routing.make({experts + 1}, kI32), map = routing.make({T * K}, kI32), ws = h.empty({(int64_t)need + 16}, kU8);
   check(fp8q_permute_pad_mxfp4(p, T, H, idx, (int32_t)K, (int32_t)experts, (int32_t)align, out<uint8_t>(q),
                                out<uint8_t>(sf), cap, out<int32_t>(off), out<int32_t>(map), ws.data_ptr(), need,
                                h.stream),

@@ -4,7 +4,8 @@ checkpoints and its backward pass, and the MXFP4 quantization and products.
 
 As in the package's other calls, the functions named ``fp8q_*`` mirror the C entry points
 argument for argument and the lower-case helpers allocate their outputs (natively, in
-csrc/moe_binding.cpp).  Both check every tensor that the caller gives (device, type,
+csrc/moe_binding.cpp; a call's small results, such as the scales of its pairs, share one
+allocation).  Both check every tensor that the caller gives (device, type,
 contiguity, size) before the library sees its address.  A helper given a ``stream``
 allocates and launches on that stream.
 """
