@@ -19,7 +19,7 @@
 // memory by bulk copies 140 us, one-shot CTAs with the loads in front 119 us).
 // The codes' scales stay out of the arithmetic (g = sg g', u = su u' with the raw codes' values
 // g', u'; the factors sg, su, w meet once per tile):
-//   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + a (1 - s) sg,  x = dy u'
+//   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + (a sg)(1 - s),  x = dy u'
 //   d gate = x slope (w su),  d up = dy a (w sg),  y = a u' (w sg su),  d w += x a (sg su).
 #include "abi_checks.h"
 #include "common.cuh"
@@ -188,7 +188,11 @@ __global__ void __launch_bounds__(kThreads, Fp8 ? 5 : 6) swiglu_bwd_kernel(BwdIn
     const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
     // exp(-g) by the hardware base-2 exponential: its argument is off by at most |g| * 2^-23,
     // far below the outputs' 8 bits.  An exponential of +inf gives s = 0.
-    const F2 k2 = make2(sg * -1.44269504f, sg * -1.44269504f), sg2 = make2(sg, sg);
+    const F2 k2 = make2(sg * -1.44269504f, sg * -1.44269504f);
+    // In the slope: a sg must not overflow where 1 - s is 0.  Above 2^118 (a stays below 2^9) every
+    // gate but 0 has s = 0 or 1, and the cap changes nothing else.
+    const float sc = fminf(sg, 0x1p118f);
+    const F2 sg2 = make2(sc, sc);
     const F2 one = make2(1.0f, 1.0f), minus = make2(-1.0f, -1.0f);
     F2 dg[8], du[8], y[8], dot = make2(0.0f, 0.0f);
 #pragma unroll
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, Fp8 ? 5 : 6) swiglu_bwd_kernel(BwdIn
       split2(add2(make2(ex2(e0), ex2(e1)), one), e0, e1);
       const F2 s = make2(rcp(e0), rcp(e1));
       const F2 act = mul2(g, s);
-      const F2 slope = fma2(mul2(act, fma2(s, minus, one)), sg2, s);  // (a sg alone can overflow)
+      const F2 slope = fma2(mul2(act, sg2), fma2(s, minus, one), s);
       const F2 x = mul2(d, u);
       dg[k] = mul2(x, slope);
       du[k] = mul2(d, act);
