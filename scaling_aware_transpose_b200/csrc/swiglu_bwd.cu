@@ -14,7 +14,7 @@
 // then a sum over the warp's lanes in a fixed order, and nothing waits for another warp.
 // Per element 4 B are read and 4 B (BF16) or 2 to 3 B (E4M3) written.  The BF16 form moves
 // them at 6.2 TB/s (86.6 us at [32768, 2048]); the E4M3 form at 4.9 TB/s (96 us), bound by
-// the issue of about 40 instructions an element at 20 warps an SM (96 registers: fewer spill,
+// the issue of about 36 instructions an element at 20 warps an SM (96 registers: fewer spill,
 // more leave too few warps; eight elements a lane took 108 us, staging through shared
 // memory by bulk copies 140 us, one-shot CTAs with the loads in front 119 us).
 // The codes' scales stay out of the arithmetic (g = sg g', u = su u' with the raw codes' values
