@@ -77,7 +77,10 @@ def test_quantize_writes_its_rows_only():
 
 
 @pytest.mark.parametrize("tokens,hidden,E,K,align", [(1, 128, 4, 2, 128), (300, 640, 8, 3, 128), (513, 256, 32, 8, 16),
-                                                     (97, 384, 5, 1, 1), (64, 128, 600, 4, 128)])
+                                                     (97, 384, 5, 1, 1), (64, 128, 600, 4, 128),
+                                                     (128, 256, 32, 8, 128), (129, 256, 32, 8, 128),
+                                                     (1024, 128, 128, 1, 4), (1024, 128, 129, 1, 4), (16, 128, 100, 64, 8), (7, 1408, 2, 1, 4096),
+                                                     (33, 7168, 31, 3, 16)])
 def test_permute(tokens, hidden, E, K, align):
     d = synthetic.moe(tokens=tokens, hidden=hidden, num_experts=E, topk=K, seed=tokens)
     x, idx = synthetic.to_torch_bf16(d["x"]), torch.from_numpy(d["topk_idx"])
@@ -94,6 +97,28 @@ def test_permute(tokens, hidden, E, K, align):
     mask = tile_scales(np.ones_like(wsf), 0) == 1
     assert np.array_equal(got[:mask.size][mask], tile_scales(wsf)[mask])
     device_status_ok()
+
+
+@pytest.mark.parametrize("tokens,E,K", [(40, 6, 4), (128, 128, 8), (128, 256, 8), (300, 9, 4)])
+def test_permute_of_repeated_and_bad_ids(tokens, E, K):
+    """A token may name an expert twice; ids out of range are reported and get no row.  Few
+    pairs (one launch) and many, as the E4M3 permute treats them."""
+    g = torch.Generator().manual_seed(tokens)
+    x = normal(tokens, 256, 3)
+    idx = torch.randint(0, E, (tokens, K), generator=g).int()
+    idx[:, 1] = idx[:, 0]
+    idx[5, 2], idx[7, 0], idx[tokens - 1, K - 1] = E, -1, 1 << 30
+    q, sf, off, rmap = sat.permute_pad_mxfp4(x.cuda(), idx.cuda(), E, 16)
+    assert sat.fp8q_last_device_status() == sat.FP8Q_ERR_DEVICE
+    _, _, off8, rmap8 = sat.permute_pad_quant(x.cuda(), idx.cuda(), E, 16)
+    assert sat.fp8q_last_device_status() == sat.FP8Q_ERR_DEVICE
+    assert torch.equal(off, off8) and torch.equal(rmap, rmap8)
+    eq, _, _ = quantized(x)
+    at = rmap.view(tokens, K).cpu().numpy()
+    want = np.zeros((int(off[-1]), 128), np.uint8)
+    for k in range(K):
+        want[at[at[:, k] >= 0, k]] = eq[at[:, k] >= 0]
+    assert np.array_equal(q[:int(off[-1])].cpu().numpy(), want)
 
 
 def test_permute_leaves_rows_behind_the_last_expert():
