@@ -27,7 +27,9 @@
 // the tensor memory is freed.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "abi_checks.h"
@@ -1017,9 +1019,12 @@ fp8q_status launch_pair(const DeviceInfo& dev, const uint8_t* aq, const uint8_t*
 //   128, 10.2 by pairs);
 //   a pair's stage takes 330 ns for twice the rows, its start 3.1 us more than a CTA's alone,
 //   a change of tiles 0.7 us (8192x4096x7168: 86 us against 102 us at 256; 2048x4096x4096: 18.2
-//   against 21.8; 1024x4096x4096: 11.9 both; 512x4096x4096: 11.2 against 9.3 at 128).  With
-//   groups, the last 256 rows of each may be half empty: pairs are left to groups of 512 rows on
-//   average.
+//   against 21.8; 1024x4096x4096: 11.9 both; 512x4096x4096: 11.2 against 9.3 at 128).
+// With groups only the capacity m is known here.  A permute's capacity exceeds its pairs by at
+// least 127 a group, so m - 127 * groups pairs are assumed, spread at random: a group without a
+// pair has no tile, one with few has one, one with many ends half a tile late on average (one
+// token to 8 of 32 experts, 2048x7168: 17.1 us at 128 by the 8 tiles expected, 20.5 at 256 by the
+// 32 of the capacity; 512 tokens to 2 of 8, 4096x4096: 22 us by pairs, 26 at 256).
 struct Variant {
   int bn, split;  // bn 0: pairs
 };
@@ -1029,10 +1034,18 @@ Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sm
   const int64_t steps = (k + kBK - 1) / kBK;
   Variant best = {256, 1};
   double least = 1e30;
+  const double pairs = grouped ? (double)m - 127.0 * groups : 0.0;
+  const double hit = grouped ? (pairs > 0 ? groups * (1.0 - std::exp(-pairs / groups)) : groups) : 0.0;
+  auto row_tiles = [&](int rows) {  // of `rows` rows
+    const int64_t all = (m + rows - 1) / rows + (grouped && rows > kBM ? groups / 2 : 0);
+    if (pairs <= 0) return all;
+    return std::min(all, (int64_t)std::ceil(std::max(hit, pairs / rows + hit / 2)));
+  };
   for (int i = 0; i < 4; ++i) {
-    const int64_t tiles = (m + kBM - 1) / kBM * ((n + kBn[i] - 1) / kBn[i]);
+    const int64_t n_tiles = (n + kBn[i] - 1) / kBn[i], tiles = row_tiles(kBM) * n_tiles;
+    const int64_t most = (m + kBM - 1) / kBM * n_tiles;  // a shared k takes CTAs for each of these
     for (int s = 1; s <= 4; s *= 2) {
-      if (s > 1 && (tiles * s > sms || s > steps || kBn[i] == 32)) break;
+      if (s > 1 && (most * s > sms || s > steps || kBn[i] == 32)) break;
       const double waves = (double)((tiles * s + sms - 1) / sms);
       double t = waves * (double)((steps + s - 1) / s) * kStage[i] + 4.0 * kBn[i] * (i == 0 ? waves : 1.0);
       const double stored = (double)(m < kBM ? m : kBM) * kBn[i];  // of a tile
@@ -1044,8 +1057,8 @@ Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sm
       }
     }
   }
-  if (!grouped || (groups <= kPairMaxGroups && m >= 512 * (int64_t)groups)) {
-    const int64_t tiles = (m + 2 * kBM - 1) / (2 * kBM) * ((n + kPairN - 1) / kPairN);
+  if (!grouped || groups <= kPairMaxGroups) {
+    const int64_t tiles = row_tiles(2 * kBM) * ((n + kPairN - 1) / kPairN);
     const double waves = (double)((tiles + sms / 2 - 1) / (sms / 2));
     if (3100 + waves * ((double)steps * 330 + (n % 8 ? 1400 : 700)) < least) best = {0, 1};
   }

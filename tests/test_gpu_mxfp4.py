@@ -271,12 +271,17 @@ def test_grouped(sizes, n):
     assert (out[rows:] == 7.0).all()
 
 
-@pytest.mark.parametrize("sizes,n,k", [([1408, 0, 1152, 640], 2048, 2304), ([128, 2048, 128, 1664], 1152, 4224),
-                                       ([2560, 0, 0], 2432, 3968)])
-def test_grouped_by_pairs(sizes, n, k):
-    """Groups whose last 256 rows are half full, empty and single-tile groups among large ones."""
+@pytest.mark.parametrize("sizes,n,k,more", [([1408, 0, 1152, 640], 2048, 2304, 300), ([128, 2048, 128, 1664], 1152, 4224, 300),
+                                            ([1408, 0, 1152, 640], 2048, 7168, 300), ([128, 2048, 128, 1664], 1152, 7168, 300),
+                                            ([2560, 0, 0], 2432, 3968, 300), ([0, 128, 128], 5120, 4736, 381),
+                                            ([128, 128, 0], 512, 4608, 381), ([0, 128, 128], 128, 2944, 40),
+                                            ([128, 128], 3328, 384, 254), ([128, 0, 0, 256], 384, 4736, 508),
+                                            ([0, 0, 0, 256], 4864, 640, 508), ([256, 128, 128], 128, 128, 0)])
+def test_grouped_by_every_kernel(sizes, n, k, more):
+    """Pairs (groups whose last 256 rows are half full, empty and single-tile groups among large
+    ones) and each tile width, alone and with k shared."""
     G, rows = len(sizes), sum(sizes)
-    cap = rows + 300
+    cap = rows + more
     aq, asf, a = operand(cap, k, rows, 2)
     bq, bsf, b = operand(G * n, k, rows + 1, 2)
     off = torch.tensor(np.cumsum([0, *sizes]), dtype=torch.int32, device="cuda")
