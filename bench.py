@@ -73,6 +73,7 @@ def kernel_sources(kind: str):
             "permute_fp8": "permute_pad_quant.cu", "ep_pack": "ep_dispatch.cu", "ep_recv": "ep_dispatch.cu",
             "permute_e512": "permute_pad_quant.cu", "permute_e4096": "permute_pad_quant.cu",
             "unpermute_fp8_k": "unpermute_unpad.cu", "router": "router.cu", "router_wide": "router.cu",
+            "router_rows": "router.cu", "mxfp4_permute_few": "mxfp4_quant.cu",
             "swiglu_stash": "swiglu_quant.cu", "swiglu_bwd": "swiglu_bwd.cu", "swiglu_bwd_quant": "swiglu_bwd.cu",
             "mxfp4_quantize": "mxfp4_quant.cu", "mxfp4_permute": "mxfp4_quant.cu", "mxfp4_matmul": "mxfp4_matmul.cu",
             "mxfp4_token": "mxfp4_matmul.cu", "mxfp4_experts": "mxfp4_matmul.cu"}[kind]
@@ -81,7 +82,7 @@ def kernel_sources(kind: str):
         extra = ["permute_common.cuh"]
     if kind.startswith("router"):
         extra = ["cluster.cuh"]
-    if kind in ("mxfp4_quantize", "mxfp4_permute"):
+    if kind in ("mxfp4_quantize", "mxfp4_permute", "mxfp4_permute_few"):
         extra = ["mxfp4.cuh", "permute_common.cuh"]
     if kind in ("mxfp4_matmul", "mxfp4_token", "mxfp4_experts"):
         extra = ["mxfp4.cuh", "bulk.cuh", "cluster.cuh"]
@@ -866,6 +867,13 @@ def run_profile(args):
         pq, psf, off, rmap = sat.permute_pad_quant(x, idx, d["num_experts"], 128)
         del x
         calls = {"unpermute_fp8_k": lambda: sat.unpermute_unpad(pq, rmap, K, None, psf)}
+    elif args.profile == "router_rows":
+        d = synthetic.moe()
+        idx = torch.from_numpy(d["topk_idx"]).cuda()
+        x = torch.zeros((idx.shape[0], 128), dtype=torch.bfloat16, device="cuda")
+        _, _, off, rmap = sat.permute_pad_quant(x, idx, d["num_experts"], 128)
+        w, rows = torch.rand(idx.shape, device="cuda"), int(off[-1])
+        calls = {"router_rows": lambda: sat.permute_row_weights(w, rmap, rows)}
     elif args.profile.startswith("router"):
         # forward and backward of a training step: the MoE workload's 32 experts, or 256 with
         # sigmoid scores and a selection bias
@@ -896,7 +904,7 @@ def run_profile(args):
         calls = {"mxfp4_quantize": lambda: sat.quantize_rowwise_mxfp4(x),
                  "mxfp4_matmul": lambda: sat.matmul_mxfp4(*a, *b),
                  "mxfp4_token": lambda: sat.matmul_mxfp4(*one, *b)}
-    elif args.profile in ("mxfp4_permute", "mxfp4_experts"):
+    elif args.profile in ("mxfp4_permute", "mxfp4_permute_few", "mxfp4_experts"):
         d = synthetic.moe(tokens=4096)
         x = synthetic.to_torch_bf16(d["x"]).cuda()
         idx, E = torch.from_numpy(d["topk_idx"]).cuda(), d["num_experts"]
@@ -904,6 +912,7 @@ def run_profile(args):
         w = sat.quantize_rowwise_mxfp4(torch.randn((E * 2048, x.shape[1]), device="cuda").to(torch.bfloat16))
         out = torch.zeros((q.shape[0], 2048), dtype=torch.bfloat16, device="cuda")
         calls = {"mxfp4_permute": lambda: sat.permute_pad_mxfp4(x, idx, E, 128),
+                 "mxfp4_permute_few": lambda: sat.permute_pad_mxfp4(x[:64], idx[:64], E, 128),
                  "mxfp4_experts": lambda: sat.matmul_mxfp4(q, sf, *w, group_offsets=off, out=out)}
     else:  # permute
         d = synthetic.moe()
@@ -932,8 +941,8 @@ def main(argv=None):
     ap.add_argument("--profile", choices=["quantize", "direct", "naive", "swiglu", "permute", "rowwise_colwise",
                                           "unpermute", "unpermute_fp8", "mx32", "permute_fp8", "mx32_quantize",
                                           "direct_grouped", "ep_pack", "ep_recv", "direct_stress", "permute_e512",
-                                          "permute_e4096", "unpermute_fp8_k", "router", "router_wide",
-                                          "swiglu_stash", "swiglu_bwd", "swiglu_bwd_quant", "mxfp4_quantize",
+                                          "permute_e4096", "unpermute_fp8_k", "router", "router_wide", "router_rows",
+                                          "mxfp4_permute_few", "swiglu_stash", "swiglu_bwd", "swiglu_bwd_quant", "mxfp4_quantize",
                                           "mxfp4_permute", "mxfp4_matmul", "mxfp4_token", "mxfp4_experts"],
                     default=None,
                     help="launch only this kernel (for ncu captures); prints no bench line")
