@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) scatter_mxfp4_kernel(const uint4* __
 // stable in (token, slot) order) while its part of x is on its way, then stores its units or
 // its padding rows (148 CTAs share those: 592 took 10.6 us for the first size below).  The first
 // CTA stores the offsets and the row ids.  On the GPU and as a call from Python: one token of 7168
-// to 8 of 32 experts 6.4 / 9.1 us against 8.6 / 11.6 by three launches, 512 tokens of 2048 to 2 of
-// 8 4.5 / 7.9 against 6.0 / 11.5.  With 256 experts ranking costs as much as the launches: 1024
+// to 8 of 32 experts 7.0 / 8.2 us against 8.6 / 11.6 by three launches, 512 tokens of 2048 to 2 of
+// 8 5.0 / 8.2 against 6.0 / 11.5.  With 256 experts ranking costs as much as the launches: 1024
 // tokens of 2048 took 21.3 us against 20.4.
 constexpr int kSmallPairs = 1024, kSmallExperts = 128, kSmallWarps = kThreads / 32;
 constexpr int kSmallPadCtas = 148;
@@ -270,6 +270,17 @@ __global__ void __launch_bounds__(kThreads) permute_small_mxfp4_kernel(
   store_units(v, n_units, first, k128, topk, rows, max_rows, q, sf);
 }
 
+// A launch that waits for the kernel before it to end.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace
 }  // namespace fp8q
 
@@ -334,10 +345,13 @@ fp8q_status fp8q_permute_pad_mxfp4(const void* x, int64_t tokens, int64_t hidden
   if (ctas > kMaxInt32) return FP8Q_ERR_SHAPE;
   const int64_t pad_ctas = std::min<int64_t>((int64_t)num_experts * pad_slots, kSmallPadCtas);
   if (hidden > 0 && tokens * topk <= kSmallPairs && num_experts <= kSmallExperts)
-    return launch_after(permute_small_mxfp4_kernel, dim3((unsigned)(scatter_ctas + pad_ctas)), kThreads, small_smem(num_experts), st,
-                        static_cast<const uint4*>(x), tokens, k128, topk_idx, (int)topk, (int)num_experts, (int)align,
-                        reinterpret_cast<uint2*>(q), sf, scatter_ctas, pad_slots, expert_offsets, row_id_map, max_out_rows,
-                        dev.status) == cudaSuccess
+    // Launched without the dependent-launch attribute: with it the CTAs crowd onto the SMs that
+    // a small product before it leaves free (189 tokens through 8 experts of 1920x2560, permute
+    // and product by turns: 22.1 us a pair with it, 14.2 without).
+    return launch_plain(permute_small_mxfp4_kernel, dim3((unsigned)(scatter_ctas + pad_ctas)), kThreads,
+                        small_smem(num_experts), st, static_cast<const uint4*>(x), tokens, k128, topk_idx, (int)topk,
+                        (int)num_experts, (int)align, reinterpret_cast<uint2*>(q), sf, scatter_ctas, pad_slots,
+                        expert_offsets, row_id_map, max_out_rows, dev.status) == cudaSuccess
                ? FP8Q_OK
                : FP8Q_ERR_CUDA;
   const fp8q_status rs =
