@@ -157,3 +157,47 @@ def test_training_step_captured():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want[k]))
     device_status_ok()
+
+
+@pytest.mark.parametrize("tokens,E,K", [(5, 8, 2), (100, 16, 4), (700, 32, 8)])
+def test_shared_buffers_keep_stream_order(tokens, E, K):
+    """Two inputs by turns through the same rows, offsets and products, with nothing in between
+    but the stream: few pairs (one plain launch before the product) and many."""
+    k, n = 512, 384
+    cap = tokens * K + E * 127
+    g = torch.Generator().manual_seed(tokens)
+    inputs = []
+    for _ in range(2):
+        logits = torch.randn((tokens, E), generator=g).cuda()
+        x = torch.randn((tokens, k), generator=g).to(torch.bfloat16).cuda()
+        inputs.append((logits, x))
+    w = sat.quantize_rowwise_mxfp4(torch.randn((E * n, k), generator=g).to(torch.bfloat16).cuda())
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    idx = torch.empty((tokens, K), dtype=torch.int32, device="cuda")
+    wt = torch.empty((tokens, K), device="cuda")
+    q, sf, ws = u8(cap, k // 2), u8(sat.fp8q_mxfp4_sf_bytes(cap, k)), u8(sat.fp8q_permute_workspace_bytes(tokens, K, E))
+    off, rmap = (torch.empty(s, dtype=torch.int32, device="cuda") for s in (E + 1, tokens * K))
+    out = torch.zeros((cap, n), dtype=torch.bfloat16, device="cuda")
+
+    def step(logits, x):
+        sat.fp8q_router_topk(logits, tokens, E, sat.ROUTER_RENORM, None, None, K, 1.0, 1.0, idx, wt, None, None, None, None, 0)
+        sat.fp8q_permute_pad_mxfp4(x, tokens, k, idx, K, E, 128, q, sf, cap, off, rmap, ws, ws.numel())
+        sat.fp8q_matmul_mxfp4(q, sf, cap, *w, n, k, off, E, out)
+        return out[rmap.long()], off.clone(), rmap.clone(), wt.clone()
+
+    want = []
+    for a in inputs:
+        want.append(step(*a))
+        torch.cuda.synchronize()
+    got = [step(*inputs[i % 2]) for i in range(30)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2])), i
+    # without the reads in between, the last step's results stand
+    for i in range(31):
+        sat.fp8q_router_topk(inputs[i % 2][0], tokens, E, sat.ROUTER_RENORM, None, None, K, 1.0, 1.0, idx, wt, None, None,
+                             None, None, 0)
+        sat.fp8q_permute_pad_mxfp4(inputs[i % 2][1], tokens, k, idx, K, E, 128, q, sf, cap, off, rmap, ws, ws.numel())
+        sat.fp8q_matmul_mxfp4(q, sf, cap, *w, n, k, off, E, out)
+    assert torch.equal(out[rmap.long()], want[0][0]) and torch.equal(off, want[0][1])
+    device_status_ok()
