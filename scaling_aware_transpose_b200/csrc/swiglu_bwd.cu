@@ -21,6 +21,8 @@
 // g', u'; the factors sg, su, w meet once per tile):
 //   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + (a sg)(1 - s),  x = dy u'
 //   d gate = x slope (w su),  d up = dy a (w sg),  y = a u' (w sg su),  d w += x a (sg su).
+#include <cfloat>
+
 #include "abi_checks.h"
 #include "common.cuh"
 #include "launch.h"
@@ -110,19 +112,17 @@ __device__ __forceinline__ float max3abs(float a, float b, float c) {
   return r;
 }
 
-// Row-wise quantization of v * factor over a tile's eight lanes x 16 values.  The factor is
-// applied to the maximum, and together with 2^-e to the values.
-__device__ __forceinline__ void quantize_store(const F2 (&v)[8], float factor, uint8_t* q, uint8_t* sf, int64_t at,
-                                               int64_t tile, int sub, bool live) {
+// Row-wise quantization of v * factor over a tile's eight lanes x 16 values: the factor is applied
+// to the tile's maximum, which gives e, and as f = factor * 2^-e to the values.
+__device__ __forceinline__ float tile_amax(const F2 (&v)[8]) {
   float x[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) split2(v[i], x[2 * i], x[2 * i + 1]);
-  float amax = fmaxf(max3abs(max3abs(x[0], x[1], x[2]), max3abs(x[3], x[4], x[5]), max3abs(x[6], x[7], x[8])),
-                     max3abs(max3abs(x[9], x[10], x[11]), max3abs(x[12], x[13], x[14]), x[15]));
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-  const int e = quick_exponent(amax * fabsf(factor));
-  const float f = factor * exp2_neg(e);
+  return fmaxf(max3abs(max3abs(x[0], x[1], x[2]), max3abs(x[3], x[4], x[5]), max3abs(x[6], x[7], x[8])),
+               max3abs(max3abs(x[9], x[10], x[11]), max3abs(x[12], x[13], x[14]), x[15]));
+}
+__device__ __forceinline__ void store_codes(const F2 (&v)[8], int e, float f, uint8_t* q, uint8_t* sf, int64_t at,
+                                            int64_t tile, int sub) {
   const F2 f2 = make2(f, f);
   uint32_t c[4];
 #pragma unroll
@@ -132,10 +132,19 @@ __device__ __forceinline__ void quantize_store(const F2 (&v)[8], float factor, u
     split2(mul2(v[2 * i + 1], f2), b0, b1);
     c[i] = __byte_perm(cvt_e4m3x2_f32(a0, a1), cvt_e4m3x2_f32(b0, b1), 0x5410);
   }
-  if (live) {
-    *reinterpret_cast<uint4*>(q + at) = make_uint4(c[0], c[1], c[2], c[3]);
-    if (sub == 0) sf[tile] = (uint8_t)(e + 127);
-  }
+  *reinterpret_cast<uint4*>(q + at) = make_uint4(c[0], c[1], c[2], c[3]);
+  if (sub == 0) sf[tile] = (uint8_t)(e + 127);
+}
+// f has to be finite: times a value of 0 it would be a NaN code.  It is not in a tile of nothing
+// but tiny values (saturated gates, gradients near the bottom of BF16) under a factor of 2 and
+// more.  2^64 of it go to the values then, exactly: f is at most 448 / 2^-149, or factor * 2^127
+// where e stopped at -127.  What is beyond fp32 even so (the factor itself, by the scales of the
+// largest gates) counts as the largest value.
+__device__ __forceinline__ void shift_up(F2 (&v)[8], float factor, int e, float& f) {
+  if (fabsf(f) <= FLT_MAX) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], make2(0x1p64f, 0x1p64f));
+  f = fminf(fmaxf(factor * 0x1p-64f * exp2_neg(e), -FLT_MAX), FLT_MAX);
 }
 
 constexpr int kThreads = 128;
@@ -217,9 +226,28 @@ __global__ void __launch_bounds__(kThreads, Fp8 ? 5 : 6) swiglu_bwd_kernel(BwdIn
       sum = __fmaf_rn((a0 + a1) * sg, su, sum);
     }
     if (Fp8) {
-      quantize_store(dg, w * su, out.dgq, out.dgsf, at, tile, sub, live);
-      quantize_store(du, w * sg, out.duq, out.dusf, at, tile, sub, live);
-      if (out.yq != nullptr) quantize_store(y, w * sg * su, out.yq, out.ysf, at, tile, sub, live);
+      // The three together: their maxima's shuffles overlap (one after the other 98.4 us, not
+      // 95.6), and one test covers the f's.
+      float mg = tile_amax(dg), mu = tile_amax(du), my = tile_amax(y);
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) {
+        mg = fmaxf(mg, __shfl_xor_sync(kAll, mg, o));
+        mu = fmaxf(mu, __shfl_xor_sync(kAll, mu, o));
+        my = fmaxf(my, __shfl_xor_sync(kAll, my, o));
+      }
+      const float cg = w * su, cu = w * sg, cy = w * sg * su;
+      const int eg = quick_exponent(mg * fabsf(cg)), eu = quick_exponent(mu * fabsf(cu)), ey = quick_exponent(my * fabsf(cy));
+      float fg = cg * exp2_neg(eg), fu = cu * exp2_neg(eu), fy = cy * exp2_neg(ey);
+      if (!(max3abs(fg, fu, fy) <= FLT_MAX)) {
+        shift_up(dg, cg, eg, fg);
+        shift_up(du, cu, eu, fu);
+        shift_up(y, cy, ey, fy);
+      }
+      if (live) {
+        store_codes(dg, eg, fg, out.dgq, out.dgsf, at, tile, sub);
+        store_codes(du, eu, fu, out.duq, out.dusf, at, tile, sub);
+        if (out.yq != nullptr) store_codes(y, ey, fy, out.yq, out.ysf, at, tile, sub);
+      }
     } else if (live) {
       const F2 fg = make2(w * su, w * su), fu = make2(w * sg, w * sg);
       uint32_t p[16];
