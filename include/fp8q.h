@@ -366,8 +366,10 @@ fp8q_status fp8q_permute_pad_quant_noalloc(const void *x, int64_t tokens, int64_
  * probability of e.
  *   logits     : fp32 [tokens, num_experts], or BF16 with FP8Q_ROUTER_BF16.  -inf switches
  *                an expert off (p = 0; it is chosen only when fewer than topk others are
- *                left, with weight 0).  NaN counts as -inf, +inf as the largest finite
- *                value.  A row of -inf alone gets ids 0..topk-1 with weights 0.
+ *                left, with weight 0), whatever its bias.  NaN counts as -inf, +inf as the
+ *                largest finite value.  Experts that are off follow by lowest id, or with
+ *                `bias` by largest bias: a row of -inf alone gets ids 0..topk-1 without a
+ *                bias, and weights 0 in either case.
  *   bias       : fp32 [num_experts], only with FP8Q_ROUTER_SIGMOID, or NULL.  A score p + bias
  *                that is NaN counts as -inf.
  *   token_mask : u8 [tokens] or NULL.  A token with 0 (padding) still gets valid ids, its

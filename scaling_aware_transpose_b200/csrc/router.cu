@@ -5,7 +5,8 @@
 //   softmax   p_e = exp(l_e - max l) / sum exp(l - max l)
 //   sigmoid   p_e = 1 / (1 + exp(-l_e))
 //   ids       the k experts of the largest l_e (softmax, and sigmoid without a bias: both
-//             are increasing in l), or of the largest p_e + bias_e; ties to the lowest id
+//             are increasing in l), or of the largest p_e + bias_e, behind which come those
+//             switched off (l_e = -inf); ties to the lowest id
 //   weights   scale * p_i, or scale * p_i / (sum of the k chosen p + 1e-20)
 // Over the tokens that token_mask keeps, with h_e = p_e (softmax) or
 // p_e / (sum of all p + 1e-20) (sigmoid):
@@ -276,8 +277,16 @@ struct Pick {
 };
 
 // The score that orders experts under a bias, in double (neighbouring scores can be closer
-// than an fp32 sum resolves), as the fp32 value and the remainder.  NaN counts as -inf.
+// than an fp32 sum resolves), as the fp32 value and the remainder.  NaN counts as -inf.  An
+// expert that its logit switches off comes below every score; among themselves these are ordered
+// by the bias.
+constexpr uint32_t kOffKey = 1u;  // (order_key(-inf) is larger)
 __device__ __forceinline__ void bias_keys(float l, float bias, uint32_t& hi, uint32_t& lo) {
+  if (l == -INFINITY) {
+    hi = kOffKey;
+    lo = order_key(bias == bias ? bias : -INFINITY);
+    return;
+  }
   const double s = 1.0 / (1.0 + exp(-(double)l)) + (double)bias;
   const float h = (float)s;
   const float r = (float)(s - (double)h);
@@ -453,8 +462,19 @@ __global__ void __launch_bounds__(kThreads, resident(VPL)) router_kernel(const T
       if (MODE == kSigmoidBias) {
         float order[VPL];
         load_row<32, VPL, float>(bias, E, lane, quads && bias_quads, order);  // (padding lanes: -inf)
+        float most = val[0];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) order[i] = fmaxf(order[i] + p[i], -INFINITY);  // (NaN counts as -inf)
+        for (int i = 1; i < VPL; ++i) most = fmaxf(most, val[i]);
+        // An expert that is off stays off the list (0 * -inf is NaN), unless all of the row's are.
+        const bool some_on = __any_sync(kAll, most > -INFINITY);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) order[i] += p[i];
+        if (some_on) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) order[i] = __fmaf_rn(val[i], 0.0f, order[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) order[i] = fmaxf(order[i], -INFINITY);  // (NaN counts as -inf)
         done = pick_listed<VPL, MODE>(order, val, bias, K, lane, picks);
       } else {
         done = pick_listed<VPL, MODE>(val, val, bias, K, lane, picks);
@@ -650,14 +670,29 @@ __global__ void __launch_bounds__(kThreads, 4) router_small_kernel(const T* __re
     if (MODE == kSigmoidBias) {
       // fp32 scores decide where they can; where some token's are too close, the warp's tokens
       // are scored in double (for every token that cost half of the kernel's time).
+      // Experts that are off count as -inf there (0 * -inf is NaN), which sets none of them before
+      // another; where a whole row is off, its biases do.
+      float score[V], most = val[0];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = expert_of<L>(sub, i);
         float p, q;
         sigmoid2(val[i], p, q);
-        const float score = e < E ? p + bias[e] : 0.0f;
-        key[i] = e < E ? order_key(score == score ? score : -INFINITY) : 0u;
+        score[i] = e < E ? p + bias[e] : 0.0f;
+        most = fmaxf(most, val[i]);
       }
+      const bool some_on = (__ballot_sync(kAll, most > -INFINITY) >> (grp * L) & ((1u << L) - 1u)) != 0u;
+      if (__all_sync(kAll, some_on)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] = __fmaf_rn(val[i], 0.0f, score[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (some_on && val[i] == -INFINITY) score[i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        key[i] = expert_of<L>(sub, i) < E ? order_key(score[i] == score[i] ? score[i] : -INFINITY) : 0u;
       if (__any_sync(kAll, choose(true) && here)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {

@@ -29,6 +29,10 @@ def router(logits, topk, sigmoid=False, renorm=True, bias=None, mask=None, scale
             h = p
     key = p + np.asarray(bias, np.float64) if bias is not None else l
     key = np.where(np.isnan(key), -np.inf, key)
+    if bias is not None:  # experts that are off come behind all others, by the bias among themselves
+        order = np.lexsort((-key, np.isneginf(l)), axis=1)
+        key = np.empty_like(key)
+        np.put_along_axis(key, order, np.broadcast_to(-np.arange(E, dtype=np.float64), (T, E)), 1)
     idx = np.argsort(-key, axis=1, kind="stable")[:, :topk]
     pk = np.take_along_axis(p, idx, 1)
     P = pk.sum(1, keepdims=True) + 1e-20 if renorm else np.ones((T, 1))
