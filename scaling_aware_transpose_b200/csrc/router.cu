@@ -277,10 +277,10 @@ struct Pick {
 };
 
 // The score that orders experts under a bias, in double (neighbouring scores can be closer
-// than an fp32 sum resolves), as the fp32 value and the remainder.  NaN counts as -inf.  An
-// expert that its logit switches off comes below every score; among themselves these are ordered
-// by the bias.
-constexpr uint32_t kOffKey = 1u;  // (order_key(-inf) is larger)
+// than an fp32 sum resolves), as the upper and the lower half of a key with the same order.  NaN
+// counts as -inf.  An expert that its logit switches off comes below every score; among
+// themselves these are ordered by the bias.
+constexpr uint32_t kOffKey = 1u;  // (the upper half of -inf's key is 0x000FFFFF)
 __device__ __forceinline__ void bias_keys(float l, float bias, uint32_t& hi, uint32_t& lo) {
   if (l == -INFINITY) {
     hi = kOffKey;
@@ -288,10 +288,10 @@ __device__ __forceinline__ void bias_keys(float l, float bias, uint32_t& hi, uin
     return;
   }
   const double s = 1.0 / (1.0 + exp(-(double)l)) + (double)bias;
-  const float h = (float)s;
-  const float r = (float)(s - (double)h);
-  hi = order_key(h == h ? h : -INFINITY);
-  lo = order_key(r == r ? r : 0.0f);
+  const uint64_t b = (uint64_t)__double_as_longlong(s == s ? s + 0.0 : -(double)INFINITY);  // (-0 counts as 0)
+  const uint64_t key = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+  hi = (uint32_t)(key >> 32);
+  lo = (uint32_t)key;
 }
 
 // Any row: each pick passes over the whole row.  Writes the k picks, best first.
@@ -389,7 +389,7 @@ __device__ __forceinline__ bool pick_listed(const float (&order)[VPL], const flo
     const uint32_t top = __reduce_max_sync(kAll, key);
     bool won = key == top;
     const unsigned b = __ballot_sync(kAll, won);
-    if (b & (b - 1u)) {  // equal keys: the remainder, then the lowest id
+    if (b & (b - 1u)) {  // equal upper halves: the lower ones, then the lowest id
       if (MODE == kSigmoidBias) {
         const uint32_t t2 = __reduce_max_sync(kAll, won ? lo : 0u);
         won = won && lo == t2;
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_small_kernel(const T* __re
 #pragma unroll
     for (int i = 0; i < V; ++i) val[i] = clean(next[i]);
     load(t + stride);
-    // ---- the k picks, by `key` (and under a bias its remainder `key_lo`).  With `check`, one
+    // ---- the k picks, by `key` (and under a bias its lower half `key_lo`).  With `check`, one
     // round more: true if two neighbours in the order may be closer than their fp32 errors.
     auto choose = [&](bool check) {
       bool close = false;

@@ -1,6 +1,7 @@
 """The router's choice under a selection bias: experts that a logit of -inf (or NaN) switches
 off come after every other, whatever their bias, in each of the kernels, on the fp32 scores'
-way and on the exact one, with few and many slots.
+way and on the exact one, with few and many slots; and scores are told apart down to the last
+bit of their double sums.
 
 The wanted ids are found here from the definition, by (off, -score, id) with the score
 1 / (1 + exp(-l)) + bias in float64; the weights' bound is that of test_gpu_router."""
@@ -113,3 +114,19 @@ def test_the_lowest_finite_logits_are_not_off():
             bias = torch.zeros(E)
             bias[3:5] = 2.0
             assert (check(l, bias, 3)[:, 0] == 3).all()
+
+
+@pytest.mark.parametrize("E,K", [(60, 8), (128, 8), (200, 8), (256, 20), (500, 16), (1000, 33)])
+def test_scores_one_bit_apart(E, K):
+    """Equal logits and biases of whole multiples of 2^-52: p + bias is exact in double (p in
+    [0.5, 1) has a last bit of 2^-53), so the multiples alone order the experts; equal ones by
+    the lowest id.  The last row's p in [2^-3, 2^-2), where twice as much of the sum lies beyond
+    a pair of fp32 values."""
+    g = torch.Generator().manual_seed(E)
+    steps = torch.randint(0, 8, (E,), generator=g)
+    want = np.lexsort((-steps.numpy(),))[:K]
+    bias = steps.double().mul(2.0 ** -52).float()
+    for x in (0.405465, 0.1, 1.7, 3.3, -1.7):
+        l = torch.full((6, E), x)
+        assert (check(l, bias, K) == want).all()
+        assert (sat.router_topk(l.cuda(), K, sigmoid=True, bias=bias.cuda())[0].cpu().numpy() == want).all()
