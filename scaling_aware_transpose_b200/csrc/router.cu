@@ -27,9 +27,9 @@
 // maximum and a vote instead of a pass over the row.  With a bias the list is made from fp32
 // scores with a margin for their rounding, and only its members are scored in double.
 // Up to 128 experts 8 or 16 lanes hold a token and a warp works on four or two.
-// All sums are fp32 in a fixed order (per lane over its tokens, over the warp's tokens, over
-// the CTA's warps, then over CTAs in double), the counts are integers: nothing depends on the
-// order of atomics.
+// All sums are fp32 in a fixed order (per lane over its tokens, at most 256 of them in a launch,
+// over the warp's tokens, over the CTA's warps, then over CTAs and launches in double), the
+// counts are integers: nothing depends on the order of atomics.
 //
 // What bounds it: the issue of instructions (ncu: 71% of the slots), about 760 a token forward
 // and 450 backward at 256 experts, three quarters of them the warp-wide rounds of the choice
@@ -204,6 +204,7 @@ struct RouterArgs {
 // parts), or with `fused` (one cluster holds every CTA) straight to the results.
 struct StatsOut {
   uint32_t* ws;
+  int64_t row, rows;  // of the parts: of this launch's first CTA, and of all launches
   int32_t* counts;
   float* prob_sums;
   float* loss;
@@ -216,14 +217,15 @@ __device__ __forceinline__ float loss_of(const RouterArgs& a, float loss_coef, d
 }
 
 // The CTA's sums and counts (complete, behind a barrier).  Workspace: [0] a counter for the
-// finishing kernel, then per CTA E sums (fp32), then per CTA E counts (int32), from byte 16 on.
+// finishing kernel, then a row per CTA of E sums (fp32), then of E counts (int32), from byte 16 on.
 __device__ __forceinline__ void publish(const float* sums, const int* counts, const RouterArgs& a, const StatsOut& out) {
   if (!out.fused) {
     float* part = reinterpret_cast<float*>(out.ws + 4);
-    int32_t* part_n = reinterpret_cast<int32_t*>(part + (int64_t)gridDim.x * a.E);
+    int32_t* part_n = reinterpret_cast<int32_t*>(part + out.rows * a.E);
+    const int64_t at = (out.row + blockIdx.x) * a.E;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
-      part[(int64_t)blockIdx.x * a.E + e] = sums[e];
-      part_n[(int64_t)blockIdx.x * a.E + e] = counts[e];
+      part[at + e] = sums[e];
+      part_n[at + e] = counts[e];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) out.ws[0] = 0u;
     return;
@@ -782,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_small_kernel(const T* __re
 // rows (10 each at most, all on their way at once), the CTAs' sums joined in rank order; the
 // last cluster to finish (the counter was zeroed by the kernel before) forms the loss.
 constexpr int kFinishCluster = 8;
-__global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, RouterArgs a, StatsOut out) {
+__global__ void __launch_bounds__(kThreads) router_finish_kernel(RouterArgs a, StatsOut out) {
   __shared__ double sum_sh[kWarps][32];
   __shared__ int cnt_sh[kWarps][32];
   __shared__ bool last;
@@ -796,6 +798,7 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, Rou
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int e = blockIdx.x / size * 32 + lane;
   const float* part = reinterpret_cast<const float*>(ws + 4);
+  const int blocks = (int)out.rows;
   const int32_t* part_n = reinterpret_cast<const int32_t*>(part + (int64_t)blocks * E);
   double s = 0.0;
   int n = 0;
@@ -1262,6 +1265,17 @@ int router_blocks(int64_t tokens, int experts) {
   const int64_t b = (tokens + tokens_per_cta(experts) - 1) / tokens_per_cta(experts);
   return (int)(b < 1 ? 1 : b < max_blocks(experts) ? b : max_blocks(experts));
 }
+// A lane adds its tokens' shares one after the other.  With statistics a launch takes 256 of them a
+// lane at most (1.2 million tokens from 129 experts on, 2.4 or 4.8 million below): one share added
+// 74000 times over, by a router that has not learned yet, would be off by 1e-3.
+constexpr int kRounds = 256;
+int64_t tokens_per_launch(int experts) { return (int64_t)kRounds * tokens_per_cta(experts) * max_blocks(experts); }
+// CTAs of all launches.
+int64_t stats_rows(int64_t tokens, int experts) {
+  const int64_t most = tokens_per_launch(experts);
+  if (tokens <= most) return router_blocks(tokens, experts);
+  return tokens / most * max_blocks(experts) + (tokens % most ? router_blocks(tokens % most, experts) : 0);
+}
 // Few tokens: up to eight CTAs, two rounds each, joined as one cluster - no second launch (64
 // tokens to 32 experts: 5.4 us on the GPU; four rounds, 1000 tokens, took 11.6 us, as much as
 // the second launch costs).
@@ -1344,7 +1358,7 @@ extern "C" {
 size_t fp8q_router_workspace_bytes(int64_t tokens, int32_t num_experts) {
   if (tokens < 0 || num_experts < 1 || num_experts > kRouterMaxExperts) return 0;
   if (fused(tokens, num_experts)) return 16;
-  return 16 + (size_t)router_blocks(tokens, num_experts) * num_experts * 8;
+  return 16 + (size_t)stats_rows(tokens, num_experts) * num_experts * 8;
 }
 
 fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_experts, uint32_t flags,
@@ -1368,24 +1382,30 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
   }
   DeviceInfo dev;
   if (device_info(&dev) != FP8Q_OK) return FP8Q_ERR_CUDA;
-  const RouterArgs a = {tokens, num_experts, topk, (flags & FP8Q_ROUTER_RENORM) != 0, stats, scale};
+  RouterArgs a = {tokens, num_experts, topk, (flags & FP8Q_ROUTER_RENORM) != 0, stats, scale};
   const int mode = !(flags & FP8Q_ROUTER_SIGMOID) ? kSoftmax : bias ? kSigmoidBias : kSigmoid;
   cudaStream_t st = to_stream(stream);
   const bool one = stats && fused(tokens, num_experts);
-  int blocks = router_blocks(tokens, num_experts);
-  if (one && blocks > kFusedCtas) blocks = kFusedCtas;
-  const StatsOut out = {static_cast<uint32_t*>(workspace), counts, prob_sums, loss, loss_coef, one};
-  const FwdPtrs p = {bias, token_mask, topk_idx, weights};
-  const cudaError_t rc =
-      (flags & FP8Q_ROUTER_BF16)
-          ? launch_fwd(mode, static_cast<const uint16_t*>(logits), p, a, out, blocks, st)
-          : launch_fwd(mode, static_cast<const float*>(logits), p, a, out, blocks, st);
-  if (rc != cudaSuccess) return FP8Q_ERR_CUDA;
+  StatsOut out = {static_cast<uint32_t*>(workspace), 0, stats ? stats_rows(tokens, num_experts) : 0,
+                  counts, prob_sums, loss, loss_coef, one};
+  const int64_t most = stats ? tokens_per_launch(num_experts) : tokens;
+  for (int64_t t = 0; t == 0 || t < tokens; t += most) {
+    a.tokens = tokens - t < most ? tokens - t : most;
+    int blocks = router_blocks(a.tokens, num_experts);
+    if (one && blocks > kFusedCtas) blocks = kFusedCtas;
+    const FwdPtrs p = {bias, token_mask ? token_mask + t : nullptr, topk_idx + t * topk, weights + t * topk};
+    const cudaError_t rc =
+        (flags & FP8Q_ROUTER_BF16)
+            ? launch_fwd(mode, static_cast<const uint16_t*>(logits) + t * num_experts, p, a, out, blocks, st)
+            : launch_fwd(mode, static_cast<const float*>(logits) + t * num_experts, p, a, out, blocks, st);
+    if (rc != cudaSuccess) return FP8Q_ERR_CUDA;
+    out.row += blocks;
+  }
   if (!stats || one) return FP8Q_OK;
   // Few rows need no cluster: 64 are one or two a warp.
-  const unsigned size = blocks > 64 ? kFinishCluster : blocks > kWarps ? 2 : 1;
-  return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st,
-                               blocks, a, out) == cudaSuccess
+  const unsigned size = out.rows > 64 ? kFinishCluster : out.rows > kWarps ? 2 : 1;
+  return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st, a,
+                               out) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }
