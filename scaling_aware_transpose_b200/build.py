@@ -22,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
 BINDING = os.path.join(PKG, "_moe_binding.so")
+BINDING_KEY = os.path.join(BUILD, "moe_binding.key")
 CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -62,9 +63,20 @@ def _compile(src):
     return obj
 
 
+def _binding_key() -> str:
+    """What the binding is compiled against: torch's C++ headers and the interpreter's."""
+    import sysconfig
+
+    import torch
+    return "\n".join(str(x) for x in (torch.__version__, torch.__file__, torch._C._GLIBCXX_USE_CXX11_ABI,
+                                      sysconfig.get_config_var("SOABI"), sysconfig.get_paths()["include"])) + "\n"
+
+
 def _build_binding(force: bool) -> None:
     src = os.path.join(CSRC, "moe_binding.cpp")
-    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__)])):
+    key = _binding_key()
+    built = open(BINDING_KEY).read() if os.path.exists(BINDING_KEY) else ""
+    if not (force or built != key or _stale(BINDING, [src, os.path.join(INCLUDE, "fp8q.h"), os.path.abspath(__file__)])):
         return
     import sysconfig
 
@@ -82,6 +94,8 @@ def _build_binding(force: bool) -> None:
     if r.returncode:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY, "w") as f:
+        f.write(key)
 
 
 def build(force: bool = False) -> str:

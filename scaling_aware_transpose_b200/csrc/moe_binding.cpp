@@ -7,6 +7,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
+#include <torch/version.h>
 
 #include <optional>
 #include <tuple>
@@ -338,6 +339,7 @@ Tensor matmul_mxfp4(const Tensor& aq, const Tensor& asf, const Tensor& bq, const
 }  // namespace
 
 PYBIND11_MODULE(_moe_binding, m) {
+  m.attr("torch_version") = TORCH_VERSION;  // its classes' layouts are compiled in
   m.def("router_topk", &router_topk);
   m.def("router_topk_bwd", &router_topk_bwd);
   m.def("permute_row_weights", &permute_row_weights);

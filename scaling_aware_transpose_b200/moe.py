@@ -74,13 +74,16 @@ def _binding():
     """The native half of the helpers (csrc/moe_binding.cpp); raises if it was not built."""
     global _native
     if _native is None:
-        import torch  # noqa: F401 - its libraries must be loaded first
+        import torch  # its libraries must be loaded first
         lib()
         try:
             from . import _moe_binding
         except ImportError as e:
             raise RuntimeError("_moe_binding.so is missing or does not load; build it with "
                                "`python -m scaling_aware_transpose_b200.build`") from e
+        if _moe_binding.torch_version != torch.__version__.split("+")[0]:
+            raise RuntimeError(f"_moe_binding.so was built for torch {_moe_binding.torch_version}, this is torch "
+                               f"{torch.__version__}; build it with `python -m scaling_aware_transpose_b200.build`")
         _native = _moe_binding
     return _native
 
