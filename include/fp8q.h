@@ -532,6 +532,12 @@ fp8q_status fp8q_debug_exp_spec_range(uint32_t first_bits, int64_t n, float *out
 fp8q_status fp8q_debug_swiglu_spec(const float *gate, const float *up, int64_t n, float *y, fp8q_stream_t stream);
 fp8q_status fp8q_debug_silu_bf16(const void *gate, int64_t n, float *y, fp8q_stream_t stream);
 
+/* Test hook (host only, no CUDA call): which kernel fp8q_matmul_mxfp4 takes for these sizes on a
+ * GPU of `sms` multiprocessors; num_groups 0 is the dense form.  *columns = columns of a tile
+ * (0: tiles of 256 x 256 by CTA pairs), *split = CTAs that share a tile's k. */
+fp8q_status fp8q_debug_mxfp4_variant(int64_t m, int64_t n, int64_t k, int32_t num_groups, int32_t sms,
+                                     int32_t *columns, int32_t *split);
+
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int fp8q_version(void);
 

@@ -91,6 +91,7 @@ def lib() -> ctypes.CDLL:
             "fp8q_quantize_rowwise_mxfp4": ([P, I64, I64, P, P, P], ctypes.c_int),
             "fp8q_permute_pad_mxfp4": ([P, I64, I64, P, I32, I32, I32, P, P, I64, P, P, P, SZ, P], ctypes.c_int),
             "fp8q_matmul_mxfp4": ([P, P, I64, P, P, I64, I64, P, I32, P, P], ctypes.c_int),
+            "fp8q_debug_mxfp4_variant": ([I64, I64, I64, I32, I32, ctypes.POINTER(I32), ctypes.POINTER(I32)], ctypes.c_int),
             "fp8q_permute_row_weights": ([P, P, I64, I64, P, P], ctypes.c_int),
             "fp8q_version": ([], ctypes.c_int),
         }

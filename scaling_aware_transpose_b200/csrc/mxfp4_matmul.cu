@@ -1070,6 +1070,16 @@ Variant choose(int64_t m, int64_t n, int64_t k, bool grouped, int groups, int sm
 
 using namespace fp8q;
 
+extern "C" fp8q_status fp8q_debug_mxfp4_variant(int64_t m, int64_t n, int64_t k, int32_t num_groups, int32_t sms,
+                                                int32_t* columns, int32_t* split) {
+  if (m < 1 || n < 1 || k < 128 || k % 128 || num_groups < 0 || sms < 2) return FP8Q_ERR_ARG;
+  if (!columns || !split) return FP8Q_ERR_NULL;
+  const Variant v = choose(m, n, k, num_groups > 0, num_groups > 0 ? num_groups : 1, sms);
+  *columns = v.bn;
+  *split = v.split;
+  return FP8Q_OK;
+}
+
 // A tile's sum over the largest k takes about 30 ms, far below the bound on the waits.
 constexpr int64_t kMaxK = 1 << 24;
 

@@ -18,7 +18,7 @@ __all__ = [
     "fp8q_router_topk_bwd", "fp8q_permute_row_weights", "router_topk", "router_topk_bwd", "permute_row_weights",
     "fp8q_swiglu_quant_stash", "fp8q_swiglu_bwd", "fp8q_swiglu_bwd_quant", "swiglu_quant_stash", "swiglu_bwd",
     "swiglu_bwd_quant", "fp8q_mxfp4_sf_bytes", "fp8q_quantize_rowwise_mxfp4", "fp8q_permute_pad_mxfp4",
-    "fp8q_matmul_mxfp4", "mxfp4_tile_scales", "quantize_rowwise_mxfp4", "permute_pad_mxfp4", "matmul_mxfp4",
+    "fp8q_matmul_mxfp4", "fp8q_debug_mxfp4_variant", "mxfp4_tile_scales", "quantize_rowwise_mxfp4", "permute_pad_mxfp4", "matmul_mxfp4",
 ]
 
 ROUTER_SIGMOID = 0x1  # FP8Q_ROUTER_SIGMOID
@@ -277,6 +277,15 @@ def fp8q_matmul_mxfp4(aq, asf, m: int, bq, bsf, n: int, k: int, group_offsets, n
         _in(bq, "bq", u8, b_rows * (k // 2), dev), _in(bsf, "bsf", u8, fp8q_mxfp4_sf_bytes(b_rows, k), dev), n, k,
         _in(group_offsets, "group_offsets", torch.int32, num_groups + 1, dev), num_groups,
         _in(out, "out", torch.bfloat16, m * n, dev), _raw_stream(stream, dev)), "fp8q_matmul_mxfp4")
+
+
+def fp8q_debug_mxfp4_variant(m: int, n: int, k: int, num_groups: int, sms: int):
+    """(columns of a tile or 0 for CTA pairs, CTAs that share a tile's k); num_groups 0: dense."""
+    import ctypes
+    columns, split = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().fp8q_debug_mxfp4_variant(m, n, k, num_groups, sms, ctypes.byref(columns), ctypes.byref(split)),
+           "fp8q_debug_mxfp4_variant")
+    return columns.value, split.value
 
 
 def mxfp4_tile_scales(sf):
