@@ -31,11 +31,10 @@
 // over the warp's tokens, over the CTA's warps, then over CTAs and launches in double), the
 // counts are integers: nothing depends on the order of atomics.
 //
-// What bounds it: the issue of instructions (ncu: 71% of the slots), about 760 a token forward
-// and 450 backward at 256 experts, three quarters of them the warp-wide rounds of the choice
-// and the sums rather than work on the logits.  50021 x 256 fp32 with a bias: 57 us forward
-// with statistics, 33 us backward, against 8 and 16 us for the bytes (passing over the row
-// for every pick: 130 us).  16384 x 32 BF16, four tokens a warp: 11.3 and 4.7 us (a warp a
+// What bounds it: the issue of instructions (ncu at 16384 x 256 with a bias: 67% of the slots in
+// both directions), about 820 a token forward and 555 backward.  50021 x 256 fp32 with a bias:
+// 56 us forward with statistics, 33 us backward, against 8 and 16 us for the bytes (passing over
+// the row for every pick: 130 us).  16384 x 32 BF16, four tokens a warp: 11.3 and 4.7 us (a warp a
 // token: 14.5 and 9), of which 5 us are the finishing launch.
 #include <cfloat>
 
@@ -203,8 +202,9 @@ struct RouterArgs {
 // Where the balance statistics go: the workspace (then router_finish_kernel sums the CTAs'
 // parts), or with `fused` (one cluster holds every CTA) straight to the results.
 struct StatsOut {
-  uint32_t* ws;
-  int64_t row, rows;  // of the parts: of this launch's first CTA, and of all launches
+  uint32_t* ws;      // [0]: a counter for the finishing kernel
+  float* sums;       // the parts: a row of E sums per CTA (of this launch on)
+  int32_t* numbers;  // and of E counts
   int32_t* counts;
   float* prob_sums;
   float* loss;
@@ -216,16 +216,13 @@ __device__ __forceinline__ float loss_of(const RouterArgs& a, float loss_coef, d
   return c > 0 ? (float)((double)loss_coef * a.E * a.topk / ((double)c * (double)c) * dot) : 0.0f;
 }
 
-// The CTA's sums and counts (complete, behind a barrier).  Workspace: [0] a counter for the
-// finishing kernel, then a row per CTA of E sums (fp32), then of E counts (int32), from byte 16 on.
+// The CTA's sums and counts (complete, behind a barrier).
 __device__ __forceinline__ void publish(const float* sums, const int* counts, const RouterArgs& a, const StatsOut& out) {
   if (!out.fused) {
-    float* part = reinterpret_cast<float*>(out.ws + 4);
-    int32_t* part_n = reinterpret_cast<int32_t*>(part + out.rows * a.E);
-    const int64_t at = (out.row + blockIdx.x) * a.E;
+    const int64_t at = (int64_t)blockIdx.x * a.E;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
-      part[at + e] = sums[e];
-      part_n[at + e] = counts[e];
+      out.sums[at + e] = sums[e];
+      out.numbers[at + e] = counts[e];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) out.ws[0] = 0u;
     return;
@@ -784,11 +781,11 @@ __global__ void __launch_bounds__(kThreads, 4) router_small_kernel(const T* __re
 // rows (10 each at most, all on their way at once), the CTAs' sums joined in rank order; the
 // last cluster to finish (the counter was zeroed by the kernel before) forms the loss.
 constexpr int kFinishCluster = 8;
-__global__ void __launch_bounds__(kThreads) router_finish_kernel(RouterArgs a, StatsOut out) {
+__global__ void __launch_bounds__(kThreads) router_finish_kernel(int blocks, RouterArgs a, StatsOut out) {
   __shared__ double sum_sh[kWarps][32];
   __shared__ int cnt_sh[kWarps][32];
   __shared__ bool last;
-  pdl_wait_for(out.ws, out.counts, out.prob_sums);
+  pdl_wait_for(out.ws, out.sums, out.numbers, out.counts, out.prob_sums);
   pdl_trigger();
   const int E = a.E;
   uint32_t* ws = out.ws;
@@ -797,9 +794,8 @@ __global__ void __launch_bounds__(kThreads) router_finish_kernel(RouterArgs a, S
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int e = blockIdx.x / size * 32 + lane;
-  const float* part = reinterpret_cast<const float*>(ws + 4);
-  const int blocks = (int)out.rows;
-  const int32_t* part_n = reinterpret_cast<const int32_t*>(part + (int64_t)blocks * E);
+  const float* part = out.sums;
+  const int32_t* part_n = out.numbers;
   double s = 0.0;
   int n = 0;
   if (e < E) {
@@ -1386,8 +1382,11 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
   const int mode = !(flags & FP8Q_ROUTER_SIGMOID) ? kSoftmax : bias ? kSigmoidBias : kSigmoid;
   cudaStream_t st = to_stream(stream);
   const bool one = stats && fused(tokens, num_experts);
-  StatsOut out = {static_cast<uint32_t*>(workspace), 0, stats ? stats_rows(tokens, num_experts) : 0,
-                  counts, prob_sums, loss, loss_coef, one};
+  // Workspace: 16 bytes, then all CTAs' rows of sums, then of counts.
+  const int64_t rows = stats ? stats_rows(tokens, num_experts) : 0;
+  float* sums = stats ? static_cast<float*>(workspace) + 4 : nullptr;
+  int32_t* numbers = stats ? reinterpret_cast<int32_t*>(sums + rows * num_experts) : nullptr;
+  StatsOut out = {static_cast<uint32_t*>(workspace), sums, numbers, counts, prob_sums, loss, loss_coef, one};
   const int64_t most = stats ? tokens_per_launch(num_experts) : tokens;
   for (int64_t t = 0; t == 0 || t < tokens; t += most) {
     a.tokens = tokens - t < most ? tokens - t : most;
@@ -1399,13 +1398,18 @@ fp8q_status fp8q_router_topk(const void* logits, int64_t tokens, int32_t num_exp
             ? launch_fwd(mode, static_cast<const uint16_t*>(logits) + t * num_experts, p, a, out, blocks, st)
             : launch_fwd(mode, static_cast<const float*>(logits) + t * num_experts, p, a, out, blocks, st);
     if (rc != cudaSuccess) return FP8Q_ERR_CUDA;
-    out.row += blocks;
+    if (stats) {
+      out.sums += (int64_t)blocks * num_experts;
+      out.numbers += (int64_t)blocks * num_experts;
+    }
   }
   if (!stats || one) return FP8Q_OK;
+  out.sums = sums;
+  out.numbers = numbers;
   // Few rows need no cluster: 64 are one or two a warp.
-  const unsigned size = out.rows > 64 ? kFinishCluster : out.rows > kWarps ? 2 : 1;
-  return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st, a,
-                               out) == cudaSuccess
+  const unsigned size = rows > 64 ? kFinishCluster : rows > kWarps ? 2 : 1;
+  return launch_clusters_after(router_finish_kernel, (unsigned)((num_experts + 31) / 32) * size, size, kThreads, 0, st,
+                               (int)rows, a, out) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }
