@@ -24,10 +24,11 @@
  *     bytes: S = 2^(byte - 127).  An all-zero tile has scale byte 127 (S = 1).
  *   - Each call is asynchronous on `stream` (NULL = the legacy default stream) and
  *     returns after the launch.  Its kernels are launched as programmatic dependent
- *     launches: their thread blocks may be placed on the GPU while the previous kernel
- *     in the stream is finishing, but none touches memory before that kernel has
- *     completed, so stream order holds as for a plain launch; a later kernel launched
- *     the same way may likewise be placed early.  Host-detectable argument errors
+ *     launches (but for fp8q_permute_pad_mxfp4 of few pairs, which starts when the
+ *     previous kernel has ended): their thread blocks may be placed on the GPU while the
+ *     previous kernel in the stream is finishing, but none touches memory before that
+ *     kernel has completed, so stream order holds as for a plain launch; a later kernel
+ *     launched the same way may likewise be placed early.  Host-detectable argument errors
  *     return before any launch and leave every output untouched.  Errors that only the
  *     device can see (bad group offsets, routing indices out of range, a bounded wait
  *     that expired) are recorded in one per-device status word; read it with
@@ -439,8 +440,8 @@ fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id
  *   drow_weights[row] = sum over the row of dy*g*s*u      (out, fp32 [rows], or NULL; only
  *                       with row_weights), summed in a fixed order.
  * fp8q_swiglu_bwd_quant: the same gradients as row-wise E4M3 pairs (dgq, dgsf), (duq, dusf)
- * by the rule of fp8q_quantize_rowwise on their fp32 values, ready for the FP8 products and
- * fp8q_direct_transpose (dense or grouped); with yq, ysf (both or neither) also y = g*s*u*w
+ * by the rule of fp8q_quantize_rowwise on their fp32 values, in the form that FP8 products
+ * (which are the caller's) and fp8q_direct_transpose (dense or grouped) take; with yq, ysf (both or neither) also y = g*s*u*w
  * recomputed from the codes, so that the forward's q need not be kept.
  *
  * All: cols % 128 == 0, any rows >= 0; codes and BF16 arrays 16-byte aligned; outputs may

@@ -18,7 +18,8 @@ constexpr uint64_t kWaitTimeoutNs = 1000000000ull;  // bounded mbarrier waits: 1
 __device__ __forceinline__ void record_status(int* status, int code) { atomicCAS(status, 0, code); }
 
 // ------------------------------------------------------------ dependent launches
-// Every kernel of the library is launched with the programmatic-stream-serialization
+// Every kernel of the library but the MXFP4 permute of few pairs (a plain launch: it starts
+// when the previous kernel has ended) is launched with the programmatic-stream-serialization
 // attribute (launch_after), so its CTAs may be scheduled while the previous kernel in the
 // stream is still finishing.  pdl_wait() returns once that previous grid has completed
 // and its writes are visible (a hardware dependency, not a spin loop); pdl_trigger() lets

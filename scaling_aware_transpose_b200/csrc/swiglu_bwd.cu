@@ -13,10 +13,11 @@
 // elements each, four tiles a pass, the next pass's loads in flight during this one.  d w is
 // then a sum over the warp's lanes in a fixed order, and nothing waits for another warp.
 // Per element 4 B are read and 4 B (BF16) or 2 to 3 B (E4M3) written.  The BF16 form moves
-// them at 6.2 TB/s (86.6 us at [32768, 2048]); the E4M3 form at 4.9 TB/s (96 us), bound by
-// the issue of about 36 instructions an element at 20 warps an SM (96 registers: fewer spill,
-// more leave too few warps; eight elements a lane took 108 us, staging through shared
-// memory by bulk copies 140 us, one-shot CTAs with the loads in front 119 us).
+// them at 6.2 TB/s (86.6 us at [32768, 2048]); the E4M3 form at 4.9 TB/s (95 us), bound by
+// the issue of about 35 instructions an element at 20 warps an SM (ncu: 71% of the slots; 96
+// registers: fewer spill more, more leave too few warps; when the form took 97 us, eight
+// elements a lane took 108 us, staging through shared memory by bulk copies 140 us, one-shot
+// CTAs with the loads in front 119 us).
 // The codes' scales stay out of the arithmetic (g = sg g', u = su u' with the raw codes' values
 // g', u'; the factors sg, su, w meet once per tile):
 //   s = 1 / (1 + 2^(g' * (-sg log2 e))),  a = g' s,  slope = s + (a sg)(1 - s),  x = dy u'
