@@ -353,7 +353,8 @@ fp8q_status fp8q_permute_pad_quant_noalloc(const void *x, int64_t tokens, int64_
 /* ------------------------------------------------------------------ router
  * The router in front of the permute: which experts a token goes to, with which weights,
  * and the balance loss that keeps them evenly used.  For logits l[t, e]:
- *   p = softmax(l[t, :]), or with FP8Q_ROUTER_SIGMOID p_e = 1 / (1 + exp(-l_e));
+ *   p = softmax(l[t, :]), or with FP8Q_ROUTER_SIGMOID p_e = 1 / (1 + exp(-l_e))  (a p
+ *     below 2^-126 counts as 0, but not in the choice);
  *   topk_idx[t, :] = the topk experts of largest l (with `bias`: of largest p_e + bias_e,
  *     formed in double), largest first, equal ones by lowest id: always distinct ids in
  *     [0, num_experts), as the permutes need them;
@@ -446,7 +447,9 @@ fp8q_status fp8q_permute_row_weights(const float *weights, const int32_t *row_id
  *
  * All: cols % 128 == 0, any rows >= 0; codes and BF16 arrays 16-byte aligned; outputs may
  * not alias inputs.  The codes must come from a quantization (never 0x7F/0xFF).  A product
- * outside fp32's range is the caller's (inputs of ordinary size have none).
+ * outside fp32's range is the caller's (inputs of ordinary size have none).  Products are
+ * formed from the codes' values before their scales: what is below 2^-126 there (a gradient
+ * below 1e-34, say, through a gate at -80 into rows of 1e6) loses digits, to 0 at worst.
  * Errors: NULL, ALIGN, SHAPE, ARG (only one of a pair, drow_weights without row_weights),
  * CUDA. */
 fp8q_status fp8q_swiglu_quant_stash(const void *gate, const void *up, const float *row_weights, int64_t rows,
