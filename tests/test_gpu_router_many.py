@@ -56,3 +56,21 @@ def test_few_rounds_and_many_agree():
     n = 2 * 75 + 256 + 14               # 2 * router_units at a span of logits below 26, and the additions
     assert ((sums - want).abs() <= n * U * want).all() and ((parts - want).abs() <= n * U * want).all()
     device_status_ok()
+
+
+def test_several_launches_under_capture():
+    """A call of two launches captured once and replayed on other logits gives the same bits."""
+    E, K, T = 160, 2, 592 * 8 * 256 + 5000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    a, b = (torch.randn((T, E), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    want = {k: [t.clone() for t in sat.router_topk(x, K)] for k, x in (("a", a), ("b", b))}
+    buf = a.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = sat.router_topk(buf, K)
+    for k, x in (("b", b), ("a", a)):
+        buf.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want[k])), k
+    device_status_ok()
